@@ -325,6 +325,222 @@ NVFP4_API int nvfp4_gemm_grouped(const void* X, int x_per_route, const int32_t* 
                                  const nvfp4_expert* experts, int E, float* Y, int64_t N, int64_t K,
                                  nvfp4_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * The paged cache of keys and values, and what works on it: rotary positions
+ * with the append of a q/k/v projection's output, attention of decode rows
+ * and drafted trees, and the page operations of beams and verification.
+ * ------------------------------------------------------------------------ */
+
+/*
+ * A paged cache, described by the caller (host struct of device pointers;
+ * nothing is allocated by the library, and a call keeps no copy of it).
+ *   k, v    bf16 [layers][pages][kv_heads][page_size][head_dim]
+ *   table   int32 [lanes][max_pages]: lane b's slot s lies in page
+ *           table[b][s / page_size] at row s % page_size.  A lane's pages come
+ *           first in its row, -1 marks the entries after them.
+ *   len     int32 [lanes]: committed slots of each lane.
+ *   ref     int32 [pages]: how many table entries name a page (plus one for
+ *           each reference of the caller's own, for a page to be kept); 0 =
+ *           free.
+ *   scratch int32 [4 * lanes + 4], zero-filled before the first call and then
+ *           left to the calls.
+ * Slots are logical positions in a lane.  Calls on one cache must be ordered
+ * (one stream, or synchronised); caches share nothing with one another.
+ *
+ * Limits (else NVFP4_ERR_SHAPE): page_size a power of two in 16..256,
+ * head_dim 64, 128 or 256, 1 <= lanes <= NVFP4_CACHE_MAX_LANES, kv_heads <=
+ * 256, pages <= 2^24, max_pages <= 2^20 with max_pages * page_size < 2^31,
+ * layers >= 1, pages * kv_heads * page_size < 2^32.  k and v 16-byte aligned,
+ * the others 4-byte (NVFP4_ERR_ALIGN); none NULL (NVFP4_ERR_ARG).
+ *
+ * What the device memory holds is checked by the kernels: a page id outside
+ * the pool, a slot without a page, a write to a page that more than one
+ * reference names, a bad parent, path or row range.  Such a row or lane is
+ * left out as each call says, and bit 128 of nvfp4_device_status() is set.
+ */
+#define NVFP4_CACHE_MAX_LANES 64
+typedef struct {
+    void* k;
+    void* v;
+    int32_t* table;
+    int32_t* len;
+    int32_t* ref;
+    int32_t* scratch;
+    int32_t layers, pages, kv_heads, page_size, head_dim, lanes, max_pages;
+    int32_t reserved;
+} nvfp4_cache;
+
+/*
+ * Every lane i takes lane parent[i]'s pages and length: beams reordered after
+ * a selection (nvfp4_beam_select's parents), sequences forked, lanes freed
+ * (parent[i] = -1: the lane is emptied).  parent: device int32 [lanes].  Only
+ * tables, lengths and reference counts change; pages are shared, and the last,
+ * partly filled one is copied by nvfp4_cache_reserve before it is written.
+ * A parent outside -1..lanes-1 counts as -1 (and sets the status bit).
+ * One asynchronous launch.
+ */
+NVFP4_API int nvfp4_cache_fork(const nvfp4_cache* cache, const int32_t* parent, nvfp4_stream_t stream);
+
+/*
+ * Room for want[b] more slots behind len[b], for every lane: pages are added
+ * where the lane has none (reference count 1), and where want[b] > 0 and the
+ * lane's last page is partly filled and shared, its filled slots are copied,
+ * in every layer, to a page of the lane's own (lanes in order; the last holder
+ * keeps the page).  Pages are taken lowest id first, lane by lane, a lane's
+ * copy before its new pages.  want: device int32 [lanes], <= 0: nothing.
+ * All or nothing: if the pool has too few free pages, or a lane would pass
+ * max_pages, nothing changes, bit 256 of nvfp4_device_status() is set and *ok
+ * is 0 (else 1).  ok: device int32, or NULL.  Two asynchronous launches.
+ */
+NVFP4_API int nvfp4_cache_reserve(const nvfp4_cache* cache, const int32_t* want, int32_t* ok, nvfp4_stream_t stream);
+
+/*
+ * Commit of drafted slots: lane b keeps count[b] of the slots behind len[b],
+ * those numbered path[b * ld_path + 0 .. count[b]) (strictly ascending, from
+ * 0: nvfp4_rope_append's rows of the lane), moved together in every layer:
+ * slot len + path[j] -> len + j.  Then len[b] += count[b], and pages wholly
+ * behind the new length lose the lane's reference.  path NULL: the first
+ * count[b] slots, as they lie.  count, path: device int32; with a path count
+ * is at most ld_path <= NVFP4_ATTN_MAX_ROWS (else NVFP4_ERR_SHAPE for ld_path;
+ * the lane is left as it was for a bad count or path, for slots without a
+ * page, and for moves into a shared page; the status bit is set).
+ * One asynchronous launch.
+ */
+NVFP4_API int nvfp4_cache_compact(const nvfp4_cache* cache, const int32_t* count, const int32_t* path, int ld_path,
+                                  nvfp4_stream_t stream);
+
+/*
+ * Lanes cut back: len[b] = min(len[b], max(new_len[b], 0)); pages wholly behind
+ * it (reserved ones too) lose the lane's reference.  new_len: device int32
+ * [lanes].  One asynchronous launch.
+ */
+NVFP4_API int nvfp4_cache_trim(const nvfp4_cache* cache, const int32_t* new_len, nvfp4_stream_t stream);
+
+/*
+ * Rotary positions and append, one asynchronous launch: row r of a q/k/v
+ * projection's FP32 output (nvfp4_gemm_decode over the stacked matrices),
+ *   y[r * ldy + ...] = q_heads x head_dim queries, kv_heads x head_dim keys,
+ *                      kv_heads x head_dim values,
+ * has its queries and keys rotated; queries go to q (bf16, row stride ldq),
+ * keys and values to `layer` of the cache (bf16) at the row's slot.
+ *
+ * Rows and lanes: row_start int32 [lanes + 1] (device): lane b has the rows
+ * row_start[b] .. row_start[b + 1) - 1, ascending from 0, and its i-th row goes
+ * to slot len[b] + i.  row_start NULL: one row per lane, row r is lane r's
+ * (rows <= lanes).  Rows at or behind row_start[lanes] are left as they were.
+ * A row whose slot has no page of the lane's own writes no keys and values
+ * (status bit 128); reserve first.  Lengths are not changed.
+ *
+ * Rotation: the first rot_dim values of a head (a multiple of 16, 0 for none)
+ * as rot_dim / 2 pairs, pair i at (i, i + rot_dim / 2) with NVFP4_ROPE_HALVES
+ * or (2i, 2i + 1) with NVFP4_ROPE_ADJACENT:
+ *   a = positions[pair_axis[i] * ldp + r] * inv_freq[i],
+ *   (x, y) -> (x cos a - y sin a, y cos a + x sin a).
+ * positions: device int32 [axes][ldp], one row per axis (a text position, or
+ * time, height and width); pair_axis: device u8 [rot_dim / 2], the axis each
+ * pair takes (values past the last axis mean the last), NULL: axis 0 for all;
+ * inv_freq: device double [rot_dim / 2].  The angle is formed and reduced in
+ * 64 bits, so far positions keep their phase; each output is rounded once.
+ *
+ * Limits: 1 <= rows (NVFP4_ERR_M), 0 <= layer < layers, 1 <= axes <= 4,
+ * q_heads a multiple of kv_heads, rot_dim <= head_dim, ldy >= the row, % 4 ==
+ * 0, ldq >= q_heads * head_dim, % 8 == 0, ldp >= rows (NVFP4_ERR_SHAPE); y and q
+ * 16-byte aligned, inv_freq 8-byte, the others 4-byte (NVFP4_ERR_ALIGN).
+ */
+enum { NVFP4_ROPE_HALVES = 0, NVFP4_ROPE_ADJACENT = 1 };
+typedef struct {
+    const nvfp4_cache* cache; /* host */
+    int32_t layer, rows, q_heads, rot_dim, style, axes;
+    const float* y;
+    int64_t ldy;
+    const int32_t* row_start;
+    const int32_t* positions;
+    int64_t ldp;
+    const uint8_t* pair_axis;
+    const double* inv_freq;
+    void* q;
+    int64_t ldq;
+} nvfp4_rope_args;
+NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stream);
+
+/*
+ * Attention of decode rows and drafted trees over the cache, one asynchronous
+ * launch.  Rows and lanes as for nvfp4_rope_append; row r, the i-th of its
+ * lane b of n rows, sees the lane's committed slots 0 .. len[b] - 1 and those
+ * drafted slots len[b] + j, j < n, whose bit j is set in mask[r] (device u64
+ * [rows]; a tree: itself and its ancestors).  mask NULL: j <= i, a chain; one
+ * row per lane is plain decode.  For query head h, with g = q_heads / kv_heads,
+ *   s_t = scale * sum_d q[r][h][d] k[t][h / g][d],
+ *   out[r][h] = sum_t exp(s_t - lse) v[t][h / g],  lse = log sum_t exp(s_t)
+ * over the visible t.  A row that sees nothing gets out = 0 and lse = -inf.
+ * What a row does not see never reaches it, infinities and NaN included; slots
+ * without a valid page are not seen (status bit 128).
+ *   q, out  bf16, row strides ldq and ldo (% 8 == 0), 16-byte aligned
+ *   lse     float [rows][q_heads], or NULL
+ * Rows at or behind row_start[lanes] are left as they were.  Sums are held in
+ * FP32; the weights exp(s - max) are rounded to bf16 for the product with v.
+ *
+ * Limits: 1 <= rows <= NVFP4_ATTN_MAX_ROWS, the verify width (NVFP4_ERR_M);
+ * q_heads a multiple of kv_heads and at most 32 times it, 0 <= layer < layers
+ * (NVFP4_ERR_SHAPE).  max_nodes: the most rows a lane is expected to have, at
+ * least 1; it only chooses the tiling.  Results are the same from call to call.
+ *
+ * workspace: device, 16-byte aligned, of nvfp4_attn_tree_workspace() bytes
+ * (else NVFP4_ERR_SCRATCH), zero-filled before its first use and then left to
+ * the calls; calls that may overlap need one each.
+ */
+#define NVFP4_ATTN_MAX_ROWS 64
+typedef struct {
+    const nvfp4_cache* cache; /* host */
+    int32_t layer, rows, q_heads, max_nodes;
+    float scale;
+    int32_t reserved;
+    const void* q;
+    int64_t ldq;
+    const int32_t* row_start;
+    const uint64_t* mask;
+    void* out;
+    int64_t ldo;
+    float* lse;
+    void* workspace;
+    uint64_t workspace_bytes;
+} nvfp4_attn_args;
+NVFP4_API int nvfp4_attn_tree(const nvfp4_attn_args* args, nvfp4_stream_t stream);
+
+/* Host helper (no GPU needed): the workspace of nvfp4_attn_tree for these sizes on a device of sm_count SMs. */
+NVFP4_API int nvfp4_attn_tree_workspace(int rows, int q_heads, int kv_heads, int head_dim, int sm_count,
+                                        size_t* bytes);
+
+/*
+ * Beam selection over the head's logits, one asynchronous launch.  `groups`
+ * groups of `beams` beams; beam w of group g is row m = g * beams + w of logits
+ * (float, row stride ldv, V columns) with the running score scores[m]:
+ *   candidate(w, v) = scores[m] + logits[m][v] - log sum_u exp(logits[m][u]),
+ * and the group's `beams` best candidates, best first, go to
+ *   scores_out[g * beams + j], parent[...] = the row m it extends, token[...] = v.
+ * Candidates are compared in 64 bits, equal ones by lower w * V + v, and the
+ * score is rounded once.  finished (u8 [rows], or NULL): a beam with a nonzero
+ * entry has one candidate, token eos at its score as it is; finished_out (u8
+ * [rows], or NULL) is 1 where the parent was finished or the token is eos.
+ * Candidates of score -inf (masked logits, beams whose score is -inf) and NaN
+ * (a row with NaN or +inf) are never taken; where fewer than `beams` are left
+ * the rest get score -inf, parent = token = -1, finished_out 0.
+ * scores_out may be scores, finished_out may be finished.
+ *
+ * Limits: groups, beams >= 1, groups * beams <= NVFP4_TOPK_MAX_ROWS
+ * (NVFP4_ERR_M); 1 <= V <= 2^20, ldv >= V, ldv % 4 == 0, and 0 <= eos < V
+ * when finished is given (NVFP4_ERR_SHAPE); logits 16-byte aligned, others by
+ * their type (NVFP4_ERR_ALIGN).  workspace: as for nvfp4_attn_tree, of
+ * nvfp4_beam_select_workspace() bytes.
+ */
+NVFP4_API int nvfp4_beam_select(const float* logits, int groups, int beams, int64_t V, int64_t ldv,
+                                const float* scores, const uint8_t* finished, int eos, float* scores_out,
+                                int32_t* parent, int32_t* token, uint8_t* finished_out, void* workspace,
+                                size_t workspace_bytes, nvfp4_stream_t stream);
+
+/* Host helper (no GPU needed): the workspace of nvfp4_beam_select for these sizes on a device of sm_count SMs. */
+NVFP4_API int nvfp4_beam_select_workspace(int groups, int beams, int64_t V, int sm_count, size_t* bytes);
+
 /*
  * Host helper (no GPU needed): the work split nvfp4_gemm_decode uses at a
  * verify width M (9..64) on a device with `sm_count` SMs -- `ctas` CTAs,
@@ -371,6 +587,10 @@ NVFP4_API int nvfp4_last_cuda_error(void);
  *   32  grouped experts: a route named an expert outside 0..E-1 or with
  *       misaligned planes (its rows are zero)
  *   64  grouped experts: a bounded wait gave up
+ *  128  paged cache: something the device memory named was refused (a page, a
+ *       slot without one, a shared page, a parent, a path, a row range)
+ *  256  paged cache: nvfp4_cache_reserve found too few free pages
+ *  512  attention: a bounded wait gave up (that call's out is wrong)
  * Reading it synchronises the device; a nonzero status also clears the flags
  * and re-zeroes the split-K counters.
  */

@@ -37,6 +37,10 @@ NVFP4_TOPK_MAX_ROWS = 64
 NVFP4_TOPK_MAX_K = 64
 NVFP4_TOPK_MAX_V = 1 << 24
 NVFP4_GROUPED_MAX_ROUTES = 128
+NVFP4_CACHE_MAX_LANES = 64
+NVFP4_ROPE_HALVES = 0
+NVFP4_ROPE_ADJACENT = 1
+NVFP4_ATTN_MAX_ROWS = 64
 NVFP4_MAX_M = 64          # nvfp4_gemm_decode: 1..8 decode lanes, 9..64 verify rows
 
 _P = ctypes.c_void_p
@@ -44,6 +48,26 @@ _I64 = ctypes.c_int64
 _SZ = ctypes.c_size_t
 _F = ctypes.c_float
 _I = ctypes.c_int
+_I32 = ctypes.c_int32
+
+
+class Nvfp4Cache(ctypes.Structure):
+    _fields_ = [("k", _P), ("v", _P), ("table", _P), ("len", _P), ("ref", _P), ("scratch", _P), ("layers", _I32),
+                ("pages", _I32), ("kv_heads", _I32), ("page_size", _I32), ("head_dim", _I32), ("lanes", _I32),
+                ("max_pages", _I32), ("reserved", _I32)]
+
+
+class Nvfp4RopeArgs(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(Nvfp4Cache)), ("layer", _I32), ("rows", _I32), ("q_heads", _I32),
+                ("rot_dim", _I32), ("style", _I32), ("axes", _I32), ("y", _P), ("ldy", _I64), ("row_start", _P),
+                ("positions", _P), ("ldp", _I64), ("pair_axis", _P), ("inv_freq", _P), ("q", _P), ("ldq", _I64)]
+
+
+class Nvfp4AttnArgs(ctypes.Structure):
+    _fields_ = [("cache", ctypes.POINTER(Nvfp4Cache)), ("layer", _I32), ("rows", _I32), ("q_heads", _I32),
+                ("max_nodes", _I32), ("scale", _F), ("reserved", _I32), ("q", _P), ("ldq", _I64), ("row_start", _P),
+                ("mask", _P), ("out", _P), ("ldo", _I64), ("lse", _P), ("workspace", _P),
+                ("workspace_bytes", ctypes.c_uint64)]
 
 
 class Nvfp4Expert(ctypes.Structure):
@@ -69,6 +93,15 @@ _SIGNATURES = {
     "nvfp4_round_destroy": (_I, [_P]),
     "nvfp4_topk": (_I, [_P, _I, _I64, _I64, _I, _P, _P, _P]),
     "nvfp4_gemm_grouped": (_I, [_P, _I, _P, _I, _I, _P, _I, _P, _I64, _I64, _P]),
+    "nvfp4_cache_fork": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P]),
+    "nvfp4_cache_reserve": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P, _P]),
+    "nvfp4_cache_compact": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P, _I, _P]),
+    "nvfp4_cache_trim": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P]),
+    "nvfp4_rope_append": (_I, [ctypes.POINTER(Nvfp4RopeArgs), _P]),
+    "nvfp4_attn_tree": (_I, [ctypes.POINTER(Nvfp4AttnArgs), _P]),
+    "nvfp4_attn_tree_workspace": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
+    "nvfp4_beam_select": (_I, [_P, _I, _I, _I64, _I64, _P, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
+    "nvfp4_beam_select_workspace": (_I, [_I, _I, _I64, _I, ctypes.POINTER(_SZ)]),
     "nvfp4_topk_splits": (_I, [_I, _I64, _I, _I, ctypes.POINTER(_I), ctypes.POINTER(_I)]),
     "nvfp4_verify_geometry": (_I, [_I, _I64, _I64, _I, ctypes.POINTER(_I64), ctypes.POINTER(_I64),
                                    ctypes.POINTER(_I)]),
@@ -199,6 +232,52 @@ def nvfp4_round_destroy(handle):
 def nvfp4_gemm_grouped(X, x_per_route, route, M, T, experts, E, Y, N, K, stream):
     return load().nvfp4_gemm_grouped(X, int(x_per_route), route, int(M), int(T), experts, int(E), Y, int(N), int(K),
                                      _s(stream))
+
+
+def nvfp4_cache_fork(cache, parent, stream):
+    return load().nvfp4_cache_fork(cache, parent, _s(stream))
+
+
+def nvfp4_cache_reserve(cache, want, ok, stream):
+    return load().nvfp4_cache_reserve(cache, want, ok, _s(stream))
+
+
+def nvfp4_cache_compact(cache, count, path, ld_path, stream):
+    return load().nvfp4_cache_compact(cache, count, path, int(ld_path), _s(stream))
+
+
+def nvfp4_cache_trim(cache, new_len, stream):
+    return load().nvfp4_cache_trim(cache, new_len, _s(stream))
+
+
+def nvfp4_rope_append(args, stream):
+    return load().nvfp4_rope_append(args, _s(stream))
+
+
+def nvfp4_attn_tree(args, stream):
+    return load().nvfp4_attn_tree(args, _s(stream))
+
+
+def nvfp4_attn_tree_workspace(rows, q_heads, kv_heads, head_dim, sm_count):
+    """(status, bytes)."""
+    n = _SZ()
+    st = load().nvfp4_attn_tree_workspace(int(rows), int(q_heads), int(kv_heads), int(head_dim), int(sm_count),
+                                          ctypes.byref(n))
+    return st, n.value
+
+
+def nvfp4_beam_select(logits, groups, beams, V, ldv, scores, finished, eos, scores_out, parent, token, finished_out,
+                      workspace, workspace_bytes, stream):
+    return load().nvfp4_beam_select(logits, int(groups), int(beams), int(V), int(ldv), scores, finished, int(eos),
+                                    scores_out, parent, token, finished_out, workspace, int(workspace_bytes),
+                                    _s(stream))
+
+
+def nvfp4_beam_select_workspace(groups, beams, V, sm_count):
+    """(status, bytes)."""
+    n = _SZ()
+    st = load().nvfp4_beam_select_workspace(int(groups), int(beams), int(V), int(sm_count), ctypes.byref(n))
+    return st, n.value
 
 
 def nvfp4_topk(logits, rows, V, ldv, k, values, indices, stream):
@@ -341,6 +420,289 @@ def topk(logits, k, V=None, values=None, indices=None, stream=None):
     check(nvfp4_topk(logits.data_ptr(), rows, V, logits.stride(0), k, values.data_ptr(), indices.data_ptr(),
                      _stream_ptr(stream)), "nvfp4_topk")
     return values, indices
+
+
+def _want(t, name, dtype, device, shape=None):
+    """Raise unless `t` is a contiguous tensor of this dtype, device and shape; its pointer (None for None)."""
+    if t is None:
+        return None
+    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and
+                                                                           tuple(t.shape) != shape):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" of shape {shape}" if shape else "") +
+                         f" on {device}: got {t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _heads(t, name, dtype, device, heads, dim):
+    """Check a [rows][heads][dim] or [rows][heads * dim] tensor whose rows are contiguous; (rows, row stride, pointer)."""
+    if t.dtype != dtype or t.device != device:
+        raise ValueError(f"{name} must be a {dtype} tensor on {device}: got {t.dtype} on {t.device}")
+    shape, stride = t.shape, t.stride()
+    flat = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
+    deep = (len(shape) == 3 and shape[1] == heads and shape[2] == dim and stride[2] == 1 and
+            (stride[1] == dim or heads == 1))
+    if not (flat or deep):
+        raise ValueError(f"{name} must be [rows][{heads}][{dim}] with contiguous rows: got {tuple(shape)} with "
+                         f"strides {stride}")
+    # a single row has no next one: its stride may be anything
+    return shape[0], (stride[0] if shape[0] > 1 else heads * dim), t.data_ptr()
+
+
+class _on_device:
+    """Make `device` current for a call and give the stream it goes to: the device's current one, or the caller's."""
+
+    def __init__(self, device, stream=None):
+        import torch
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+        self.index, self.back, self.cuda = device.index, None, torch.cuda
+        self.ptr = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+
+    def __enter__(self):
+        now = self.cuda.current_device()
+        if now != self.index:
+            self.back = now
+            self.cuda.set_device(self.index)
+        return self.ptr
+
+    def __exit__(self, *exc):
+        if self.back is not None:
+            self.cuda.set_device(self.back)
+        return False
+
+
+class Cache:
+    """A paged cache of keys and values (nvfp4_cache): the tensors and the
+    description the calls take.
+
+    k, v: bfloat16 [layers][pages][kv_heads][page_size][head_dim]; table: int32
+    [lanes][max_pages]; len: int32 [lanes]; ref: int32 [pages].  The tensors stay
+    the caller's to read and to write between calls."""
+
+    def __init__(self, k, v, table, len, ref):
+        import torch
+        dev = k.device
+        if dev.type != "cuda":
+            raise ValueError(f"the cache must be in device memory: got {dev}")
+        if k.dim() != 5 or table.dim() != 2:
+            raise ValueError("k and v must be [layers][pages][kv_heads][page_size][head_dim], table [lanes][max_pages]")
+        layers, pages, heads, page, dim = k.shape
+        lanes, width = table.shape
+        i32 = torch.int32
+        kp = _want(k, "k", torch.bfloat16, dev)
+        vp = _want(v, "v", torch.bfloat16, dev, tuple(k.shape))
+        tp = _want(table, "table", i32, dev)
+        lp = _want(len, "len", i32, dev, (lanes,))
+        rp = _want(ref, "ref", i32, dev, (pages,))
+        self.k, self.v, self.table, self.len, self.ref = k, v, table, len, ref
+        self.device, self.lanes, self.kv_heads, self.head_dim, self.page_size = dev, lanes, heads, dim, page
+        self.scratch = torch.zeros(4 * lanes + 4, dtype=i32, device=dev)
+        self.c = Nvfp4Cache(kp, vp, tp, lp, rp, self.scratch.data_ptr(), layers, pages, heads, page, dim, lanes, width, 0)
+        self._ref = ctypes.byref(self.c)
+
+    @classmethod
+    def empty(cls, layers, pages, kv_heads, page_size, head_dim, lanes, max_pages, device):
+        """A cache with every page free and every lane empty."""
+        import torch
+        shape = (layers, pages, kv_heads, page_size, head_dim)
+        dev = torch.device(device)
+        if dev.type == "cuda" and dev.index is None:
+            dev = torch.device("cuda", torch.cuda.current_device())
+        i32 = torch.int32
+        return cls(torch.zeros(shape, dtype=torch.bfloat16, device=dev),
+                   torch.zeros(shape, dtype=torch.bfloat16, device=dev),
+                   torch.full((lanes, max_pages), -1, dtype=i32, device=dev),
+                   torch.zeros(lanes, dtype=i32, device=dev), torch.zeros(pages, dtype=i32, device=dev))
+
+    def _lanes(self, t, name):
+        import torch
+        return _want(t, name, torch.int32, self.device, (self.lanes,))
+
+    def fork(self, parent, stream=None):
+        """Lane i takes lane parent[i]'s pages and length (-1: emptied)."""
+        pp = self._lanes(parent, "parent")
+        with _on_device(self.device, stream) as s:
+            check(load().nvfp4_cache_fork(self._ref, pp, s), "nvfp4_cache_fork")
+
+    def reserve(self, want, ok=None, stream=None):
+        """Room for want[b] more slots in each lane; shared last pages are copied.
+        ok: int32 [1], set to 0 if the pool had too few free pages."""
+        import torch
+        wp, op = self._lanes(want, "want"), _want(ok, "ok", torch.int32, self.device, (1,))
+        with _on_device(self.device, stream) as s:
+            check(load().nvfp4_cache_reserve(self._ref, wp, op, s), "nvfp4_cache_reserve")
+
+    def compact(self, count, path=None, stream=None):
+        """Commit count[b] drafted slots of each lane, those numbered path[b][:count[b]] (None: the first ones)."""
+        import torch
+        cp, pp, ld = self._lanes(count, "count"), None, 1
+        if path is not None:
+            pp = _want(path, "path", torch.int32, self.device)
+            if path.dim() != 2 or path.shape[0] != self.lanes:
+                raise ValueError(f"path must be [{self.lanes}][n]: got {tuple(path.shape)}")
+            ld = path.shape[1]
+        with _on_device(self.device, stream) as s:
+            check(load().nvfp4_cache_compact(self._ref, cp, pp, ld, s), "nvfp4_cache_compact")
+
+    def trim(self, new_len, stream=None):
+        """Cut lanes back to new_len[b] slots."""
+        np_ = self._lanes(new_len, "new_len")
+        with _on_device(self.device, stream) as s:
+            check(load().nvfp4_cache_trim(self._ref, np_, s), "nvfp4_cache_trim")
+
+
+def rope_args(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, style=NVFP4_ROPE_HALVES, row_start=None,
+              q=None):
+    """(Nvfp4RopeArgs, q) of a rotary append; see rope_append."""
+    import torch
+    dev, dim = cache.device, cache.head_dim
+    rows, ldy, yp = _heads(y, "y", torch.float32, dev, q_heads + 2 * cache.kv_heads, dim)
+    if q is None:
+        q = torch.empty((rows, q_heads, dim), dtype=torch.bfloat16, device=dev)
+    qrows, ldq, qp = _heads(q, "q", torch.bfloat16, dev, q_heads, dim)
+    if qrows != rows:
+        raise ValueError(f"q has {qrows} rows, y {rows}")
+    half = 0 if inv_freq is None else inv_freq.numel()
+    axes, ldp, pp = 1, rows, None
+    if half:
+        pp = _want(positions, "positions", torch.int32, dev)
+        if positions is None or positions.dim() > 2 or positions.shape[-1] != rows:
+            raise ValueError(f"positions must be [{rows}] or [axes][{rows}]")
+        axes = 1 if positions.dim() == 1 else positions.shape[0]
+    sp = _want(row_start, "row_start", torch.int32, dev, (cache.lanes + 1,))
+    ap = _want(pair_axis, "pair_axis", torch.uint8, dev, (half,))
+    fp = _want(inv_freq, "inv_freq", torch.float64, dev, (half,)) if half else None
+    return Nvfp4RopeArgs(ctypes.pointer(cache.c), layer, rows, q_heads, 2 * half, style, axes, yp, ldy, sp, pp, ldp, ap,
+                         fp, qp, ldq), q
+
+
+def rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, style=NVFP4_ROPE_HALVES,
+                row_start=None, q=None, stream=None):
+    """Rotate the queries and keys of y (float32 [rows][(q_heads + 2 kv_heads) * head_dim], the q/k/v projection's
+    output) and append keys and values to `layer` of the cache; returns q bfloat16 [rows][q_heads][head_dim].
+
+    inv_freq: float64 [rot_dim / 2] (None: no rotation); positions: int32 [rows] or [axes][rows]; pair_axis: uint8
+    [rot_dim / 2]; row_start: int32 [lanes + 1], or None for one row per lane."""
+    if stream is not None:  # what is allocated here belongs to the stream that uses it
+        import torch
+        with torch.cuda.stream(stream):
+            return rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
+    a, q = rope_args(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
+    with _on_device(cache.device) as s:
+        check(load().nvfp4_rope_append(ctypes.byref(a), s), "nvfp4_rope_append")
+    return q
+
+
+_sms = {}
+
+
+def _sm_count(device):
+    import torch
+    if device.index not in _sms:
+        _sms[device.index] = torch.cuda.get_device_properties(device).multi_processor_count
+    return _sms[device.index]
+
+
+def attn_tree_workspace(cache, rows, q_heads):
+    """A zero-filled workspace for attn_tree calls of these sizes (uint8)."""
+    import torch
+    st, n = nvfp4_attn_tree_workspace(rows, q_heads, cache.kv_heads, cache.head_dim, _sm_count(cache.device))
+    check(st, "nvfp4_attn_tree_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+
+
+def attn_args(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, out=None, want_lse=False, lse=None,
+              workspace=None):
+    """(Nvfp4AttnArgs, out, lse, workspace) of an attention call; see attn_tree."""
+    import torch
+    dev, dim = cache.device, cache.head_dim
+    heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // dim
+    rows, ldq, qp = _heads(q, "q", torch.bfloat16, dev, heads, dim)
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
+    orows, ldo, op = _heads(out, "out", torch.bfloat16, dev, heads, dim)
+    if orows != rows:
+        raise ValueError(f"out has {orows} rows, q {rows}")
+    if lse is None and want_lse:
+        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+    sp = _want(row_start, "row_start", torch.int32, dev, (cache.lanes + 1,))
+    mp = _want(mask, "mask", torch.int64, dev, (rows,))
+    ep = _want(lse, "lse", torch.float32, dev, (rows, heads))
+    if workspace is None:
+        workspace = attn_tree_workspace(cache, rows, heads)
+    wp = _want(workspace, "workspace", torch.uint8, dev)
+    return Nvfp4AttnArgs(ctypes.pointer(cache.c), layer, rows, heads, max_nodes, scale, 0, qp, ldq, sp, mp, op, ldo, ep,
+                         wp, workspace.numel()), out, lse, workspace
+
+
+def attn_tree(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, out=None, want_lse=False, lse=None,
+              workspace=None, stream=None):
+    """Attention of decode rows or drafted trees over `layer` of the cache: out bfloat16 [rows][q_heads][head_dim], or
+    (out, lse float32 [rows][q_heads]) if lse is given or wanted.
+
+    q: bfloat16 [rows][q_heads][head_dim]; row_start: int32 [lanes + 1], or None for one row per lane; mask: int64
+    [rows], bit j of a row's word set where it sees its lane's j-th drafted slot (None: a chain); workspace: from
+    attn_tree_workspace, one for each stream or graph whose calls may overlap (None: a new one)."""
+    if stream is not None:  # what is allocated here belongs to the stream that uses it
+        import torch
+        with torch.cuda.stream(stream):
+            return attn_tree(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
+    a, out, lse, workspace = attn_args(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
+    with _on_device(cache.device) as s:
+        check(load().nvfp4_attn_tree(ctypes.byref(a), s), "nvfp4_attn_tree")
+    return out if lse is None else (out, lse)
+
+
+def beam_select_workspace(groups, beams, vocab, device):
+    """A zero-filled workspace for beam_select calls of these sizes (uint8)."""
+    import torch
+    st, n = nvfp4_beam_select_workspace(groups, beams, vocab, _sm_count(torch.device(device)))
+    check(st, "nvfp4_beam_select_workspace")
+    return torch.zeros(n, dtype=torch.uint8, device=device)
+
+
+def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=None, parent=None, token=None,
+                finished_out=None, workspace=None, stream=None):
+    """The best continuations of each group of beams: (scores float32, parent int32, token int32, finished uint8), each
+    [groups][beams], best first.
+
+    logits: float32 [groups * beams][>= vocab], rows contiguous; scores: float32 [groups][beams]; finished: uint8
+    [groups][beams] with its end token eos; parent is the row of logits that is extended (what Cache.fork takes)."""
+    import torch
+    if stream is not None:  # what is allocated here belongs to the stream that uses it
+        with torch.cuda.stream(stream):
+            return beam_select(logits, scores, vocab, finished, eos, scores_out, parent, token, finished_out, workspace)
+    dev = logits.device
+    if dev.type != "cuda":
+        raise ValueError(f"logits must be in device memory: got {dev}")
+    groups, beams = scores.shape
+    if logits.dim() != 2 or logits.shape[0] != groups * beams or logits.dtype != torch.float32 or \
+            (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits must be float32 [{groups * beams}][vocab] with contiguous rows")
+    V = logits.shape[1] if vocab is None else int(vocab)
+    if V > logits.shape[1]:
+        raise ValueError(f"vocab {V} is past the logits' {logits.shape[1]} columns")
+    ldv = logits.stride(0) if groups * beams > 1 else (max(logits.stride(0), V) + 3) // 4 * 4
+    f32, i32, u8 = torch.float32, torch.int32, torch.uint8
+    shape = (groups, beams)
+    if scores_out is None:
+        scores_out = torch.empty(shape, dtype=f32, device=dev)
+    if parent is None:
+        parent = torch.empty(shape, dtype=i32, device=dev)
+    if token is None:
+        token = torch.empty(shape, dtype=i32, device=dev)
+    if finished_out is None:
+        finished_out = torch.empty(shape, dtype=u8, device=dev)
+    if workspace is None:
+        workspace = beam_select_workspace(groups, beams, V, dev)
+    ptr = (_want(scores, "scores", f32, dev, shape), _want(finished, "finished", u8, dev, shape),
+           _want(scores_out, "scores_out", f32, dev, shape), _want(parent, "parent", i32, dev, shape),
+           _want(token, "token", i32, dev, shape), _want(finished_out, "finished_out", u8, dev, shape),
+           _want(workspace, "workspace", u8, dev))
+    with _on_device(dev) as s:
+        check(load().nvfp4_beam_select(logits.data_ptr(), groups, beams, V, ldv, ptr[0], ptr[1], eos, ptr[2], ptr[3],
+                                       ptr[4], ptr[5], ptr[6], workspace.numel(), s), "nvfp4_beam_select")
+    return scores_out, parent, token, finished_out
 
 
 def stream_read(buf, ctas, out=None, stream=None):

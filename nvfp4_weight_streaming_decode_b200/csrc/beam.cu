@@ -1,0 +1,412 @@
+// beam.cu -- beam selection over the head's logits: log-softmax of every row,
+// the running scores added, and the best candidates of each group of beams,
+// in one launch that reads the logits once.
+//
+// Within a row candidates rank as their logits do, so no row needs more than
+// its `beams` largest logits, and its normaliser: row m is cut into S slices,
+// one CTA each, which keeps its slice in registers, takes its maximum, the sum
+// of exp(x - max) and its `beams` best (value, index).  The last CTA of a group
+// to finish (counter, acquire/release) joins the normalisers in slice order and
+// ranks the group's beams * S * beams candidates by 64-bit scores.
+//
+// Selecting k of n values, in a slice and in the merge alike: the k-th largest
+// of the 256 threads' own maxima bounds the answer from below (k different
+// elements reach it), and few elements lie above it, so one more pass collects
+// those and each counts how many rank before it.  When ties push more than
+// kListCap elements over the bound, k rounds of a block-wide maximum decide.
+#include <cuda_runtime.h>
+#include <stdint.h>
+
+#include "cache.cuh"
+#include "internal.h"
+
+namespace nvfp4 {
+
+namespace {
+
+constexpr int kBeamThreads = 256;
+constexpr int kPerThread = 32;                          // logits a thread holds
+constexpr int kSliceMax = kBeamThreads * kPerThread;    // 8192
+constexpr int kListCap = 512;
+constexpr int kMaxRows = NVFP4_TOPK_MAX_ROWS;
+
+struct SlicePart {
+    double sum;  // of exp(x - top)
+    float top;   // -inf: the slice has nothing finite
+    float unused;
+};
+
+struct BeamParams {
+    const float* logits;
+    long long ldv;
+    int V, groups, beams, S, slice;
+    const float* scores;
+    const uint8_t* finished;
+    int eos;
+    float* scores_out;
+    int32_t *parent, *token;
+    uint8_t* finished_out;
+    SlicePart* part;    // [rows][S]
+    float* cand_x;      // [rows][S][beams]
+    int32_t* cand_v;    // their columns, -1: none
+    unsigned* counters; // [groups]
+};
+
+// An order on (value, place): the larger value first, equal ones by lower place.
+template <class T>
+__device__ __forceinline__ bool before(T a, uint32_t ia, T b, uint32_t ib)
+{
+    return a > b || (a == b && ia < ib);
+}
+
+template <class T>
+struct ListShared {
+    T top[kBeamThreads];
+    T val[kListCap];
+    uint32_t place[kListCap];
+    T wval[kBeamThreads / 32];
+    uint32_t wplace[kBeamThreads / 32];
+    T bound;
+    int count;
+};
+
+// The k best of the block's elements under `before`, to emit(rank, value,
+// place).  each(f) calls f(value, place) for the calling thread's elements,
+// which all are finite or +inf (callers leave out -inf and NaN); `mine` is the
+// thread's largest, or -inf.  Returns how many there are, at most k.
+template <class T, class Each, class Emit>
+__device__ int block_best(int k, T mine, T none, Each each, Emit emit, ListShared<T>& sh)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    sh.top[tid] = mine;
+    if (tid == 0) {
+        sh.bound = none;
+        sh.count = 0;
+    }
+    __syncthreads();
+    // this thread's place among the threads' maxima; the k-th one bounds the answer
+    int rank = 0;
+    for (int i = 0; i < kBeamThreads; ++i) {
+        const T o = sh.top[i];
+        rank += o > mine || (o == mine && i < tid);
+    }
+    if (rank == k - 1) sh.bound = mine;
+    __syncthreads();
+    const T bound = sh.bound;  // none: fewer than k threads hold elements, take all
+    each([&](T v, uint32_t place) {
+        if (v >= bound) {
+            const int pos = atomicAdd(&sh.count, 1);
+            if (pos < kListCap) {
+                sh.val[pos] = v;
+                sh.place[pos] = place;
+            }
+        }
+    });
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kListCap) {
+        for (int i = tid; i < n; i += kBeamThreads) {
+            const T v = sh.val[i];
+            const uint32_t p = sh.place[i];
+            int r = 0;
+            for (int j = 0; j < n; ++j) r += before(sh.val[j], sh.place[j], v, p);
+            if (r < k) emit(r, v, p);
+        }
+        __syncthreads();
+        return n < k ? n : k;
+    }
+    // many ties: one winner a round, each below the one before
+    T last = none;
+    uint32_t lastp = 0;
+    for (int r = 0; r < k; ++r) {
+        T bv = none;
+        uint32_t bp = 0xFFFFFFFFu;
+        each([&](T v, uint32_t place) {
+            if ((r == 0 || before(last, lastp, v, place)) && before(v, place, bv, bp)) {
+                bv = v;
+                bp = place;
+            }
+        });
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) {
+            const T ov = __shfl_xor_sync(0xffffffffu, bv, off);
+            const uint32_t op = __shfl_xor_sync(0xffffffffu, bp, off);
+            if (before(ov, op, bv, bp)) {
+                bv = ov;
+                bp = op;
+            }
+        }
+        if (lane == 0) {
+            sh.wval[warp] = bv;
+            sh.wplace[warp] = bp;
+        }
+        __syncthreads();
+        bv = sh.wval[0];
+        bp = sh.wplace[0];
+        for (int w = 1; w < kBeamThreads / 32; ++w)
+            if (before(sh.wval[w], sh.wplace[w], bv, bp)) {
+                bv = sh.wval[w];
+                bp = sh.wplace[w];
+            }
+        __syncthreads();
+        if (tid == 0) emit(r, bv, bp);  // n > kListCap >= k: a round never comes up empty
+        last = bv;
+        lastp = bp;
+    }
+    __syncthreads();
+    return k;
+}
+
+__global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
+{
+    __shared__ union {
+        ListShared<float> f;
+        ListShared<double> d;
+    } sh;
+    __shared__ float s_w[kBeamThreads / 32];
+    __shared__ double s_d[kBeamThreads / 32];
+    __shared__ double s_lse[kMaxRows];
+    __shared__ int s_last;
+    pdl_begin();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int s = blockIdx.x, m = blockIdx.y, g = m / p.beams;
+    const float kNone = __int_as_float(0xff800000);
+    const bool done = p.finished && p.finished[m] != 0;
+    const long long at = (long long)m * p.S + s;
+    if (!done) {
+        // 1. the slice, thread t holding columns lo + 4 t + 1024 i + (0..3)
+        const int lo = s * p.slice, n = min(p.slice, p.V - lo);
+        const float* x = p.logits + (long long)m * p.ldv + lo;
+        float r[kPerThread];
+#pragma unroll
+        for (int i = 0; i < kPerThread / 4; ++i) {
+            const int q = 4 * tid + 4 * kBeamThreads * i;
+            float4 v = make_float4(kNone, kNone, kNone, kNone);
+            if (q + 4 <= n) {
+                v = __ldcs(reinterpret_cast<const float4*>(x + q));
+            } else if (q < n) {
+                v.x = x[q];
+                if (q + 1 < n) v.y = x[q + 1];
+                if (q + 2 < n) v.z = x[q + 2];
+            }
+            r[4 * i] = v.x;
+            r[4 * i + 1] = v.y;
+            r[4 * i + 2] = v.z;
+            r[4 * i + 3] = v.w;
+        }
+        // 2. the slice's maximum and sum of exp(x - maximum): pairs in 32 bits
+        // within a thread, 64 bits across threads (the joined normaliser is
+        // then good to about 1e-8, which keeps near ties of different beams in
+        // their order)
+        float mine = kNone;
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) mine = fmaxf(mine, r[i]);
+        float top = mine;
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+        if (lane == 0) s_w[warp] = top;
+        __syncthreads();
+        top = s_w[0];
+#pragma unroll
+        for (int w = 1; w < kBeamThreads / 32; ++w) top = fmaxf(top, s_w[w]);
+        const float ref = top == kNone ? 0.f : top;  // nothing but -inf (or NaN, which the sum keeps)
+        float e[kPerThread];
+#pragma unroll
+        for (int i = 0; i < kPerThread; ++i) e[i] = expf(r[i] - ref);
+#pragma unroll
+        for (int w = kPerThread / 2; w > 0; w >>= 1)
+#pragma unroll
+            for (int i = 0; i < w; ++i) e[i] += e[i + w];
+        double sum = (double)e[0];
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) s_d[warp] = sum;
+        __syncthreads();
+        if (tid == 0) {
+            for (int w = 1; w < kBeamThreads / 32; ++w) sum += s_d[w];
+            p.part[at].sum = sum;
+            p.part[at].top = top;
+        }
+        // 3. the slice's best
+        float* cx = p.cand_x + at * p.beams;
+        int32_t* cv = p.cand_v + at * p.beams;
+        const int got = block_best<float>(
+            p.beams, mine, kNone,
+            [&](auto f) {
+#pragma unroll
+                for (int i = 0; i < kPerThread; ++i)
+                    if (r[i] > kNone) f(r[i], (uint32_t)(lo + 4 * tid + 4 * kBeamThreads * (i / 4) + i % 4));
+            },
+            [&](int rank, float v, uint32_t place) {
+                cx[rank] = v;
+                cv[rank] = (int32_t)place;
+            },
+            sh.f);
+        if (tid >= got && tid < p.beams) cv[tid] = -1;
+    }
+    // 4. the group's last CTA merges
+    __syncthreads();
+    if (tid == 0) s_last = count_in(p.counters + g) == (unsigned)(p.beams * p.S - 1);
+    __syncthreads();
+    if (!s_last) return;
+    for (int w = warp; w < p.beams; w += kBeamThreads / 32) {
+        const long long row = (long long)(g * p.beams + w) * p.S;
+        const bool over = p.finished && p.finished[g * p.beams + w] != 0;
+        double top = -INFINITY;
+        if (!over)
+            for (int i = lane; i < p.S; i += 32) top = fmax(top, (double)__ldcg(&p.part[row + i].top));
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, off));
+        double sum = 0.0;
+        if (!over)
+            for (int i = lane; i < p.S; i += 32)
+                sum += __ldcg(&p.part[row + i].sum) * exp((double)__ldcg(&p.part[row + i].top) - top);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        if (lane == 0) s_lse[w] = top + log(sum);
+    }
+    __syncthreads();
+    const int per = p.S * p.beams, n = p.beams * per;
+    const double dnone = -INFINITY;
+    // candidate i of the group: its 64-bit score (none: not one) and w * V + v
+    auto cand = [&](int i, double& key, uint32_t& place) {
+        const int w = i / per, q = i - w * per, row = g * p.beams + w;
+        const double cum = (double)p.scores[row];
+        key = dnone;
+        if (p.finished && p.finished[row] != 0) {
+            place = (uint32_t)w * (uint32_t)p.V + (uint32_t)p.eos;
+            if (q == 0) key = cum;
+        } else {
+            const int v = __ldcg(p.cand_v + (long long)row * per + q);
+            place = (uint32_t)w * (uint32_t)p.V + (uint32_t)(v < 0 ? 0 : v);
+            if (v >= 0) key = cum + ((double)__ldcg(p.cand_x + (long long)row * per + q) - s_lse[w]);
+        }
+        if (!(key > dnone)) key = dnone;  // NaN too
+    };
+    double mine = dnone;
+    for (int i = tid; i < n; i += kBeamThreads) {
+        double key;
+        uint32_t place;
+        cand(i, key, place);
+        mine = fmax(mine, key);
+    }
+    const int o = g * p.beams;
+    __shared__ float o_score[kMaxRows];
+    __shared__ int o_parent[kMaxRows], o_token[kMaxRows], o_done[kMaxRows];
+    const int got = block_best<double>(
+        p.beams, mine, dnone,
+        [&](auto f) {
+            for (int i = tid; i < n; i += kBeamThreads) {
+                double key;
+                uint32_t place;
+                cand(i, key, place);
+                if (key > dnone) f(key, place);
+            }
+        },
+        [&](int rank, double key, uint32_t place) {
+            const int w = (int)(place / (uint32_t)p.V), v = (int)(place - (uint32_t)w * (uint32_t)p.V);
+            o_score[rank] = (float)key;
+            o_parent[rank] = o + w;
+            o_token[rank] = v;
+            o_done[rank] = v == p.eos || (p.finished && p.finished[o + w] != 0);
+        },
+        sh.d);
+    // scores and finished may be the outputs' own memory: written when all is read
+    if (tid < p.beams) {
+        const bool real = tid < got;
+        p.scores_out[o + tid] = real ? o_score[tid] : kNone;
+        p.parent[o + tid] = real ? o_parent[tid] : -1;
+        p.token[o + tid] = real ? o_token[tid] : -1;
+        if (p.finished_out) p.finished_out[o + tid] = real ? (uint8_t)o_done[tid] : 0;
+    }
+    if (tid == 0) p.counters[g] = 0u;
+}
+
+struct BeamSplit {
+    int S, slice;
+    size_t part, x, v, counters, bytes;  // offsets into the workspace
+};
+
+int beam_split(int groups, int beams, int64_t V, int sms, BeamSplit* b)
+{
+    if (groups < 1 || beams < 1 || groups > kMaxRows || beams > kMaxRows || groups * beams > kMaxRows)
+        return NVFP4_ERR_M;
+    if (V < 1 || V > (1 << 20)) return NVFP4_ERR_SHAPE;
+    const int rows = groups * beams;
+    // Slices of at most kSliceMax, otherwise two CTAs per SM over all rows, at
+    // least 1024 logits each.
+    int64_t S = (V + kSliceMax - 1) / kSliceMax;
+    int64_t want = (2LL * sms + rows - 1) / rows;
+    const int64_t most = (V + 1023) / 1024;
+    if (want > most) want = most;
+    if (S < want) S = want;
+    int64_t slice = (V + S - 1) / S;
+    slice = (slice + 3) / 4 * 4;
+    b->S = (int)((V + slice - 1) / slice);
+    b->slice = (int)slice;
+    auto up = [](size_t x) { return (x + 255) / 256 * 256; };
+    const size_t cells = (size_t)rows * b->S;
+    b->counters = 0;
+    b->part = up(sizeof(unsigned) * kMaxRows);
+    b->x = b->part + up(cells * sizeof(SlicePart));
+    b->v = b->x + up(cells * beams * sizeof(float));
+    b->bytes = b->v + up(cells * beams * sizeof(int32_t));
+    return NVFP4_OK;
+}
+
+}  // namespace
+}  // namespace nvfp4
+
+using namespace nvfp4;
+
+extern "C" int nvfp4_beam_select_workspace(int groups, int beams, int64_t V, int sm_count, size_t* bytes)
+{
+    if (!bytes || sm_count < 1) return NVFP4_ERR_ARG;
+    BeamSplit b;
+    const int st = beam_split(groups, beams, V, sm_count, &b);
+    if (st == NVFP4_OK) *bytes = b.bytes;
+    return st;
+}
+
+extern "C" int nvfp4_beam_select(const float* logits, int groups, int beams, int64_t V, int64_t ldv,
+                                 const float* scores, const uint8_t* finished, int eos, float* scores_out,
+                                 int32_t* parent, int32_t* token, uint8_t* finished_out, void* workspace,
+                                 size_t workspace_bytes, cudaStream_t stream)
+{
+    if (!logits || !scores || !scores_out || !parent || !token || !workspace) return NVFP4_ERR_ARG;
+    BeamSplit b;
+    int st = beam_split(groups, beams, V, 1, &b);  // the limits, before any CUDA call
+    if (st != NVFP4_OK) return st;
+    if (ldv < V || ldv > ((int64_t)1 << 40) || (finished && (eos < 0 || eos >= V))) return NVFP4_ERR_SHAPE;
+    if (!aligned16(logits) || (ldv & 3) || !aligned16(workspace) ||
+        (((uintptr_t)scores | (uintptr_t)scores_out | (uintptr_t)parent | (uintptr_t)token) & 3))
+        return NVFP4_ERR_ALIGN;
+    int sms = 0;
+    st = sm_count(&sms);
+    if (st != NVFP4_OK) return st;
+    beam_split(groups, beams, V, sms, &b);
+    if (workspace_bytes < b.bytes) return NVFP4_ERR_SCRATCH;
+    BeamParams p;
+    p.logits = logits;
+    p.ldv = ldv;
+    p.V = (int)V;
+    p.groups = groups;
+    p.beams = beams;
+    p.S = b.S;
+    p.slice = b.slice;
+    p.scores = scores;
+    p.finished = finished;
+    p.eos = eos;
+    p.scores_out = scores_out;
+    p.parent = parent;
+    p.token = token;
+    p.finished_out = finished_out;
+    uint8_t* w = (uint8_t*)workspace;
+    p.counters = (unsigned*)(w + b.counters);
+    p.part = (SlicePart*)(w + b.part);
+    p.cand_x = (float*)(w + b.x);
+    p.cand_v = (int32_t*)(w + b.v);
+    NVFP4_CUDA_TRY(launch_pdl(beam_kernel, dim3((unsigned)b.S, (unsigned)(groups * beams)), dim3(kBeamThreads), 0,
+                              stream, p));
+    return NVFP4_OK;
+}

@@ -94,4 +94,21 @@ int read_and_clear_verify_status(unsigned* status);
 // Status word of the grouped expert kernel (1 = an invalid route, 2 = a bounded wait gave up).
 int read_and_clear_grouped_status(unsigned* status);
 
+// Paged cache: host-side check of a caller's description (every field, before
+// any CUDA call), and the status words of the kernels that work on one.
+int check_cache(const nvfp4_cache* c);
+int read_and_clear_cache_status(unsigned* status);  // 1 = refused content, 2 = too few free pages
+int read_and_clear_rope_status(unsigned* status);   // 1 = refused content
+int read_and_clear_attn_status(unsigned* status);   // 1 = refused content, 4 = a bounded wait gave up
+
+// Rotary append and attention as the round launches them (`pdl` as for
+// launch_gemm; arguments validated by the caller), and their argument checks.
+int validate_rope(const nvfp4_rope_args* a);
+int launch_rope(const nvfp4_rope_args* a, cudaStream_t stream);
+int validate_attn(const nvfp4_attn_args* a);
+int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream);
+
+// SM count of the current device (asked once per device).
+int sm_count(int* out);
+
 }  // namespace nvfp4
