@@ -1,15 +1,53 @@
-// attn.cu -- attention of decode rows and drafted trees over the paged cache.
+// attn.cu -- attention of decode rows and drafted trees over the paged cache,
+// on the fifth-generation tensor cores.
 //
-// For a query row the scores over the visible slots pass through a softmax
-// held as a running maximum and sum, so keys and values are read once:
-//   m' = max(m, s),  l' = l e^(m - m') + e^(s - m'),  o' = o e^(m - m') + e^(s - m') v.
-// One CTA per (row, query head); each of its warps takes every fourth slot and
-// the warps' states are joined at the end.
+// A lane's T rows times the G query heads that share a cached head form one
+// block of up to N = 16..128 query rows against the same keys and values, so
+// those are read once for all of them.  Per tile of 128 slots
+//     S^T [128 slots][N] = K Q^T        (A = K as it lies in the cache, B = Q)
+//     P^T = exp2(S^T c - m),            l += column sums (per thread, joined at the end)
+//     O^T [D][N] += V^T P^T             (A = V as it lies, read transposed, B = P)
+// with S^T and O^T in tensor memory.  Slots are the 128 rows of the first
+// product and head values those of the second, so few query rows cost few
+// columns instead of a padded tile of rows: one row and eight drafts run the
+// same code at the same memory rate.
+//
+// The reference m of a column is the maximum of the first tile that shows it a
+// slot, not the running maximum: weights up to 2^kHeadroom are as exact in
+// FP32 and bf16 as weights below 1 (both hold powers of two that far), so
+// O^T is rescaled only when a score passes m by more than that -- rarely, by a
+// vote of the 128 threads that share the columns.
+//
+// Split: the tiles of all (lane, cached head) pairs form one line that the
+// grid's CTAs share evenly (ragged lanes balance by themselves).  A pair cut
+// between CTAs leaves partial (m, l, O) in the workspace, and the last CTA to
+// finish joins them in CTA order.  Lanes with more than N query rows have
+// their blocks on neighbouring CTAs in step, so that the second reader of a
+// tile finds it in L2.
+//
+// A CTA (one per SM): eight softmax warps (two per 32 slots, half the columns
+// each), a warp that fetches pages with TMA (128-byte swizzle; K of tile t + 1
+// before V of tile t), a thread that issues the products (S of tile t + 1
+// before O of tile t, so the tensor cores work while the softmax does).
+//
+// What a row must not see: the score is replaced, not weighted, so masked keys
+// can hold anything; a masked value would still enter as 0 * NaN, so the rows
+// of V behind the last slot or of a bad page are zeroed in shared memory, and
+// non-finite values of drafted slots are zeroed there and added back at the
+// end to the rows that do see them.
+//
+// Every wait is bounded; one that runs out flags the device status, stops the
+// CTA, waits (bounded) for copies and products in flight, frees the tensor
+// memory and returns.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <math.h>
 #include <stdint.h>
 
+#include <atomic>
+
+#include "async.cuh"
 #include "cache.cuh"
 #include "internal.h"
 
@@ -19,86 +57,868 @@ __device__ unsigned int g_attn_status;
 
 namespace {
 
+constexpr unsigned kBadPage = 1u, kGaveUp = 4u;
+constexpr int kTile = 128;                 // slots per tile
+constexpr int kSoftWarps = 8;
+constexpr int kSoftThreads = kSoftWarps * 32;
+constexpr int kLoadWarp = 8, kMmaWarp = 9;
+constexpr int kAttnThreads = 320;
+constexpr int kMaxLanes = NVFP4_CACHE_MAX_LANES;
+constexpr float kHeadroom = 32.f;          // weights up to 2^32 before a rescale; their sums stay far below 2^127
+constexpr float kUnseen = -3.0e38f;        // reference of a column that has seen no slot
+constexpr uint32_t kSleepNs = 1000;
+constexpr uint32_t kPolls = 1u << 20;      // about a second
+
+// Shared-memory plan of a variant.  The ring's entries are 128 slots x up to
+// 128 values of K or V, as atoms of 128 slots x 64 values (128 bytes a slot).
+template <int D, int N>
+struct Plan {
+    static constexpr int kAtoms = D >= 128 ? 2 : 1;          // atoms per ring entry
+    static constexpr int kEntry = kAtoms * kTile * 128;      // bytes
+    static constexpr int kPer = D > 128 ? 2 : 1;             // entries per tile of K (or V)
+    static constexpr int kPBufs = N == 128 ? 1 : 2;
+    static constexpr int kPBytes = kTile * N * 2;
+    static constexpr int kQBytes = N * D * 2;
+    static constexpr int kBudget = 226 * 1024 - 8192;        // what is left holds barriers and the lane tables
+    static constexpr int kFit = (kBudget - kQBytes - kPBufs * kPBytes) / kEntry;
+    static constexpr int kRing = kFit > 12 ? 12 : kFit;
+    static constexpr int kOffP = kRing * kEntry;
+    static constexpr int kOffQ = kOffP + kPBufs * kPBytes;
+    static constexpr int kOffMisc = kOffQ + kQBytes;
+    static constexpr int kCols = N / 2;                      // columns per softmax thread
+    static constexpr int kOBlocks = D > 128 ? 2 : 1;         // 128-row blocks of O^T
+    // loads and products take entries in one order, so a tile of V beside one entry of K is enough to go on
+    static_assert(kRing > kPer, "V of a tile fits the ring");
+    static_assert(2 * N + kOBlocks * N <= 512, "tensor memory");
+};
+
+struct Shared {  // at kOffMisc
+    uint64_t full[12], empty[12];
+    uint64_t sfull[2], sfree[2], pfull[2], pfree[2];
+    uint64_t qfull, ofull, drain;
+    uint32_t tmem;
+    int abort, last, unused;
+    unsigned long long bad_v;          // drafted slots with non-finite values, this segment
+    int tiles[kMaxLanes], lo[kMaxLanes], nrow[kMaxLanes], len[kMaxLanes], end[kMaxLanes];
+    int base[kMaxLanes + 1];           // first unit of each lane
+    int width;                         // CTAs that share a (lane, head), one per block of query rows
+    uint64_t vis[128];                 // drafted slots each column sees
+    float m[128], l[128];
+    float red[4][128];
+};
+static_assert(sizeof(Shared) <= 8192 - 1024, "room for the tables, and for aligning the buffers");
+
 struct AttnParams {
     nvfp4_cache c;
     nvfp4_attn_args a;
+    float* part_o;       // [ctas][2][N][D]
+    float2* part_ml;     // [ctas][2][N]
+    unsigned* counters;  // [ctas]
+    int min_tiles;       // tiles a CTA takes at least (but for the last ones)
 };
 
-template <int D>
-__global__ void __launch_bounds__(128) attn_kernel(const AttnParams p)
+// -------------------------------------------------------------- tensor cores
+
+// K-major operand, 128-byte swizzle: 8-row groups of 128-byte rows, 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t addr)
 {
-    constexpr int kPer = D / 32;
-    __shared__ float s_m[4], s_l[4], s_o[4][D];
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// MN-major operand, 128-byte swizzle: rows of k, 64 values of mn each; the next
+// 64 values `mn_step` bytes on, the next 8 rows of k 1024 bytes on.
+__device__ __forceinline__ uint64_t desc_mn(uint32_t addr, uint32_t mn_step)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(mn_step >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+}
+// MN-major operand without swizzle: 8 x 16-byte core matrices (8 rows of k, 8
+// values of mn), the next 8 rows of k 128 bytes on, the next 8 values of mn
+// 128 slots x 16 bytes on.
+__device__ __forceinline__ uint64_t desc_p(uint32_t addr)
+{
+    return (uint64_t)((addr >> 4) & 0x3FFFu) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(kTile * 16 >> 4) << 32) |
+           ((uint64_t)1 << 46);
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
+        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        : "memory");
+}
+__device__ __forceinline__ void commit(uint32_t bar)
+{
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 8 columns of this warp's 32 lanes.
+__device__ __forceinline__ void tm_ld8(uint32_t t, float* v)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(t)
+                 : "memory");
+}
+__device__ __forceinline__ void tm_ld16(uint32_t t, float* v)
+{
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(t)
+        : "memory");
+}
+__device__ __forceinline__ void tm_st8(uint32_t t, const float* v)
+{
+    const uint32_t* r = reinterpret_cast<const uint32_t*>(v);
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(t), "r"(r[0]),
+                 "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+__device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+template <int C>
+__device__ __forceinline__ void tm_ld(uint32_t t, float (&v)[C])
+{
+    if constexpr (C == 8) {
+        tm_ld8(t, v);
+    } else {
+#pragma unroll
+        for (int i = 0; i < C; i += 16) tm_ld16(t + i, v + i);
+    }
+    tm_wait_ld();
+}
+
+__device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
+                                         uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(row), "r"(head), "r"(page), "r"(bar)
+        : "memory");
+}
+
+// ----------------------------------------------------------- bounded waits
+
+// One thread.
+__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    for (uint32_t it = 0; it < kPolls; ++it) {
+        if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
+        if (*abort) return false;
+    }
+    return false;
+}
+// A whole warp.
+__device__ __forceinline__ bool waitw(uint32_t bar, uint32_t parity, volatile int* abort)
+{
+    for (uint32_t it = 0; it < kPolls; ++it) {
+        if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kSleepNs))) return true;
+        if (__any_sync(0xffffffffu, *abort != 0)) return false;
+    }
+    return false;
+}
+__device__ __forceinline__ void give_up(volatile int* abort)
+{
+    if (!*abort) {
+        *abort = 1;
+        atomicOr(&g_attn_status, kGaveUp);
+    }
+}
+
+// Barrier over `n` threads that tells each whether any of them said yes.
+__device__ __forceinline__ bool any_of(int id, int n, bool yes)
+{
+    uint32_t r;
+    asm volatile(
+        "{\n .reg .pred p, q;\n setp.ne.b32 p, %1, 0;\n barrier.cta.red.or.pred q, %2, %3, p;\n"
+        " selp.u32 %0, 1, 0, q;\n}"
+        : "=r"(r)
+        : "r"((uint32_t)yes), "r"(id), "r"(n)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ float fast_exp2(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// ------------------------------------------------------------- the schedule
+
+// Units are (lane, cached head, tile), lane by lane; a group of `width` CTAs
+// (one per block of query rows) takes a contiguous range of them.
+struct Segment {
+    int b, h;         // lane and cached head
+    int t0, t1;       // tiles
+    int first;        // the pair's first unit
+};
+
+__device__ __forceinline__ Segment segment_at(const Shared& s, int lanes, int u, int u1)
+{
+    Segment g;
+    int b = 0;
+    while (b + 1 < lanes && s.base[b + 1] <= u) ++b;
+    const int r = u - s.base[b], n = s.tiles[b];
+    g.b = b;
+    g.h = r / n;
+    g.t0 = r - g.h * n;
+    g.first = s.base[b] + g.h * n;
+    g.t1 = min(n, g.t0 + (u1 - u));
+    return g;
+}
+
+// Position in the order of loads of a segment of n tiles: K0, K1, V0, K2, V1, ...
+__device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
+__device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
+
+// ---------------------------------------------------------------- the kernel
+
+template <int D, int N>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+    attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
+                const __grid_constant__ CUtensorMap map_v)
+{
+    using L = Plan<D, N>;
+    constexpr int C = L::kCols;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    Shared& s = *reinterpret_cast<Shared*>(sm + L::kOffMisc);
+    const uint32_t ring = smem_addr(sm), pbuf = ring + L::kOffP, qbuf = ring + L::kOffQ;
     const nvfp4_cache& c = p.c;
     const nvfp4_attn_args& a = p.a;
-    pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int h = blockIdx.x, row = blockIdx.y;
-    int b = -1, i = 0, n = 0;
-    for (int l = 0; l < c.lanes; ++l) {
-        int lo, hi;
-        lane_rows(a.row_start, l, a.rows, lo, hi);
-        if (row >= lo && row < hi) {
-            b = l;
-            i = row - lo;
-            n = hi - lo;
-            break;
-        }
-    }
-    if (b < 0) return;
+    const int G = a.q_heads / c.kv_heads;
     const int shift = __ffs(c.page_size) - 1;
-    const int len = max(c.len[b], 0);
-    const uint64_t mask = a.mask ? a.mask[row] : (i >= 63 ? ~0ull : (2ull << i) - 1);
-    const int kh = h / (a.q_heads / c.kv_heads);
-    const __nv_bfloat16* q = (const __nv_bfloat16*)a.q + (int64_t)row * a.ldq + (int64_t)h * D;
-    float qr[kPer], o[kPer];
-    for (int e = 0; e < kPer; ++e) {
-        qr[e] = __bfloat162float(q[lane + 32 * e]) * a.scale;
-        o[e] = 0.f;
-    }
-    float m = -INFINITY, l = 0.f;
-    const int64_t end = (int64_t)len + n;
-    for (int64_t s = warp; s < end; s += 4) {
-        if (s >= len && !((mask >> (s - len)) & 1)) continue;
-        const int64_t col = s >> shift;
-        const int pg = col < c.max_pages ? c.table[(int64_t)b * c.max_pages + col] : -1;
-        if (pg < 0 || pg >= c.pages) {
-            if (lane == 0) atomicOr(&g_attn_status, 1u);
-            continue;
+    volatile int* abort = &s.abort;
+
+    if (tid == 0) {
+        for (int i = 0; i < 12; ++i) {
+            mbar_init(smem_addr(&s.full[i]), 1);
+            mbar_init(smem_addr(&s.empty[i]), 1);
         }
-        const int64_t at =
-            ((((int64_t)a.layer * c.pages + pg) * c.kv_heads + kh) * c.page_size + (s & (c.page_size - 1))) * D;
-        const __nv_bfloat16* k = (const __nv_bfloat16*)c.k + at;
-        const __nv_bfloat16* v = (const __nv_bfloat16*)c.v + at;
-        float x = 0.f;
-        for (int e = 0; e < kPer; ++e) x += qr[e] * __bfloat162float(k[lane + 32 * e]);
-        for (int off = 16; off > 0; off >>= 1) x += __shfl_xor_sync(0xffffffffu, x, off);
-        const float mn = fmaxf(m, x);
-        const float w = x == -INFINITY ? 0.f : expf(x - mn), f = m == -INFINITY ? 0.f : expf(m - mn);
-        l = l * f + w;
-        for (int e = 0; e < kPer; ++e) o[e] = o[e] * f + w * __bfloat162float(v[lane + 32 * e]);
-        m = mn;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s.sfull[i]), 1);
+            mbar_init(smem_addr(&s.sfree[i]), kSoftWarps);
+            mbar_init(smem_addr(&s.pfull[i]), kSoftWarps);
+            mbar_init(smem_addr(&s.pfree[i]), 1);
+        }
+        mbar_init(smem_addr(&s.qfull), kSoftWarps);
+        mbar_init(smem_addr(&s.ofull), 1);
+        mbar_init(smem_addr(&s.drain), 1);
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_l[warp] = l;
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
     }
-    for (int e = 0; e < kPer; ++e) s_o[warp][lane + 32 * e] = o[e];
+    if (warp == kLoadWarp && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+    }
+    pdl_begin();
+    // the lanes: rows, lengths, tiles
+    if (tid < kMaxLanes) {
+        int lo = 0, hi = 0, len = 0, end = 0, tiles = 0;
+        if (tid < c.lanes) {
+            lane_rows(a.row_start, tid, a.rows, lo, hi);
+            const int64_t cap = (int64_t)c.max_pages << shift;
+            const int64_t n = max(c.len[tid], 0);
+            len = (int)(n < cap ? n : cap);
+            const int64_t e = n + (hi - lo);
+            end = (int)(e < cap ? e : cap);
+            if (hi > lo) {
+                tiles = (end + kTile - 1) / kTile;
+                if (e > cap && blockIdx.x == 0) atomicOr(&g_attn_status, kBadPage);
+            }
+        }
+        s.lo[tid] = lo;
+        s.nrow[tid] = (hi - lo) * G;
+        s.len[tid] = len;
+        s.end[tid] = end;
+        s.tiles[tid] = tiles;
+    }
     __syncthreads();
-    float top = -INFINITY, sum = 0.f, f[4];
-    for (int w = 0; w < 4; ++w) top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < 4; ++w) {
-        f[w] = s_m[w] == -INFINITY ? 0.f : expf(s_m[w] - top);
-        sum += s_l[w] * f[w];
+    if (warp == 0) {
+        // prefix sums of units and the widest lane, two lanes per thread
+        const int x0 = s.tiles[2 * lane] * c.kv_heads, x1 = s.tiles[2 * lane + 1] * c.kv_heads;
+        int incl = x0 + x1, most = max(s.nrow[2 * lane], s.nrow[2 * lane + 1]);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+        }
+        s.base[2 * lane] = incl - x0 - x1;
+        s.base[2 * lane + 1] = incl - x1;
+        if (lane == 31) s.base[kMaxLanes] = incl;
+        if (lane == 0) s.width = max(1, (most + N - 1) / N);
     }
-    const bool any = !(sum == 0.f);
-    for (int e = tid; e < D; e += 128) {
-        float acc = 0.f;
-        for (int w = 0; w < 4; ++w)
-            if (f[w] != 0.f) acc += s_o[w][e] * f[w];
-        ((__nv_bfloat16*)a.out)[(int64_t)row * a.ldo + (int64_t)h * D + e] = __float2bfloat16(any ? acc / sum : 0.f);
+    fence_after();
+    __syncthreads();
+    const uint32_t tmem = s.tmem;
+    const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
+    // this CTA's range and its block of query rows
+    const int units = s.base[kMaxLanes], width = s.width;
+    int groups = gridDim.x / width;
+    if (groups > (units + p.min_tiles - 1) / p.min_tiles) groups = (units + p.min_tiles - 1) / p.min_tiles;
+    const int group = blockIdx.x / width, blk = blockIdx.x % width;
+    const bool idle = units == 0 || group >= groups;
+    const int u0 = idle ? 0 : (int)((int64_t)units * group / groups);
+    const int u1 = idle ? 0 : (int)((int64_t)units * (group + 1) / groups);
+
+    if (warp == kLoadWarp) {
+        // ---- pages -> ring
+        int idx = 0;  // entries issued so far
+        int done = 0;
+        bool ok = true;
+        const int box = min(c.page_size, kTile);         // slots per copy
+        const int pieces = kTile / box;                  // copies per atom of a tile
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s, c.lanes, u, u1);
+            u += g.t1 - g.t0;
+            if (blk * N >= s.nrow[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
+            const int end = s.end[g.b];
+            // lane i < pieces holds the page of piece i; one tile ahead for K
+            auto page_of = [&](int t) {
+                const int slot = (g.t0 + t) * kTile + lane * box;
+                return lane < pieces && slot < end ? row[slot >> shift] : -1;
+            };
+            auto fetch = [&](const CUtensorMap* map, int pg, int t, int pos) {
+                const bool good = pg >= 0 && pg < c.pages;
+                const unsigned have = __ballot_sync(0xffffffffu, good);
+                const int off = ((g.t0 + t) * kTile + lane * box) & (c.page_size - 1);
+                for (int e = 0; e < L::kPer; ++e) {
+                    const int q = idx + pos * L::kPer + e, slot = q % L::kRing;
+                    if (q >= L::kRing && !waitw(smem_addr(&s.empty[slot]), ((q / L::kRing) - 1) & 1, abort)) return false;
+                    const uint32_t bar = smem_addr(&s.full[slot]);
+                    if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(have) * L::kAtoms * box * 128));
+                    __syncwarp();
+                    if (good) {
+                        const uint32_t dst = ring + slot * L::kEntry + lane * box * 128;
+#pragma unroll
+                        for (int x = 0; x < L::kAtoms; ++x)
+                            tma_page(dst + x * kTile * 128, map, e * 128 + x * 64, off, g.h, pg, bar);
+                    }
+                    done = q + 1;
+                }
+                return true;
+            };
+            int prev = page_of(0), next = n > 1 ? page_of(1) : -1;
+            ok = fetch(&map_k, prev, 0, 0);
+            for (int t = 1; ok && t < n; ++t) {
+                const int cur = next;
+                if (t + 1 < n) next = page_of(t + 1);
+                ok = fetch(&map_k, cur, t, pos_k(t)) && fetch(&map_v, prev, t - 1, pos_v(t - 1, n));
+                prev = cur;
+            }
+            ok = ok && fetch(&map_v, prev, n - 1, pos_v(n - 1, n));
+            idx += 2 * n * L::kPer;
+        }
+        if (!ok) {
+            if (lane == 0) give_up(abort);
+            // copies in flight: the last ring's worth of entries
+            for (int q = max(0, done - L::kRing); q < done; ++q)
+                warp_wait(smem_addr(&s.full[q % L::kRing]), (q / L::kRing) & 1);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- the products, issued by one thread
+        if (lane == 0) {
+            constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+            constexpr uint32_t kIdS = kBase, kIdO = kBase | (1u << 15) | (1u << 16);
+            int idx = 0, seg = 0;
+            int done = 0;  // tiles of earlier segments
+            bool ok = true;
+            for (int u = u0; ok && u < u1;) {
+                const Segment g = segment_at(s, c.lanes, u, u1);
+                u += g.t1 - g.t0;
+                if (blk * N >= s.nrow[g.b]) continue;
+                const int n = g.t1 - g.t0;
+                ok = wait1(smem_addr(&s.qfull), seg & 1, abort);
+                fence_after();
+                for (int t = 0; ok && t <= n; ++t) {
+                    if (t < n) {  // S of tile t
+                        const int T = done + t, sb = T & 1;
+                        if (T >= 2) ok = wait1(smem_addr(&s.sfree[sb]), ((T >> 1) - 1) & 1, abort);
+                        for (int e = 0; ok && e < L::kPer; ++e) {
+                            const int q = idx + pos_k(t) * L::kPer + e, slot = q % L::kRing;
+                            ok = wait1(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
+                            if (!ok) break;
+                            fence_after();
+#pragma unroll
+                            for (int x = 0; x < L::kAtoms; ++x)
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma(tm_s + sb * N, desc_k(ring + slot * L::kEntry + x * kTile * 128 + k * 32),
+                                        desc_k(qbuf + (e * L::kAtoms + x) * N * 128 + k * 32), kIdS, (e | x | k) != 0);
+                            commit(smem_addr(&s.empty[slot]));
+                        }
+                        if (ok) commit(smem_addr(&s.sfull[sb]));
+                    }
+                    if (ok && t > 0) {  // O of tile t - 1
+                        const int T = done + t - 1, pb = T % L::kPBufs;
+                        ok = wait1(smem_addr(&s.pfull[pb]), (T / L::kPBufs) & 1, abort);
+                        for (int e = 0; ok && e < L::kPer; ++e) {
+                            const int q = idx + pos_v(t - 1, n) * L::kPer + e, slot = q % L::kRing;
+                            ok = wait1(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
+                            if (!ok) break;
+                            fence_after();
+#pragma unroll
+                            for (int k = 0; k < kTile / 16; ++k)
+                                // head_dim 64: both halves of the 128 rows read the one atom
+                                mma(tm_o + e * N, desc_mn(ring + slot * L::kEntry + k * 2048, L::kAtoms == 2 ? kTile * 128 : 0),
+                                    desc_p(pbuf + pb * L::kPBytes + k * 256), kIdO, t > 1 || k != 0);
+                            commit(smem_addr(&s.empty[slot]));
+                        }
+                        if (ok) {
+                            commit(smem_addr(&s.pfree[pb]));
+                            if (t == n) commit(smem_addr(&s.ofull));
+                        }
+                    }
+                }
+                idx += 2 * n * L::kPer;
+                done += n;
+                ++seg;
+            }
+            if (!ok) {
+                give_up(abort);
+                commit(smem_addr(&s.drain));
+                for (uint32_t it = 0; it < kPolls && !mbar_try_wait_sleep(smem_addr(&s.drain), 0, kSleepNs); ++it) {
+                }
+            }
+        }
+        __syncwarp();
+    } else if (warp < kSoftWarps) {
+        // ---- softmax: thread = slot (and value row of O^T), half the columns
+        const int wg = warp >> 2, quad = warp & 3, srow = quad * 32 + lane, c0 = wg * C;
+        const uint32_t lanebits = (uint32_t)(quad * 32) << 16;
+        const float sl = a.scale * 1.4426950408889634f;
+        const int bar = 1 + wg;
+        int seg = 0, done = 0, idx = 0;
+        bool fail = false;
+        for (int u = u0; u < u1;) {
+            const Segment g = segment_at(s, c.lanes, u, u1);
+            u += g.t1 - g.t0;
+            if (blk * N >= s.nrow[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            const int len = s.len[g.b], end = s.end[g.b], rows = min(N, s.nrow[g.b] - blk * N), lo = s.lo[g.b];
+            const int32_t* trow = c.table + (int64_t)g.b * c.max_pages;
+            int pg = g.t0 * kTile + srow < end ? trow[(g.t0 * kTile + srow) >> shift] : -1;
+            // Q: row r of the block is query row lo + r / G, head h G + r % G
+            for (int i = tid; i < N * D / 8; i += kSoftThreads) {
+                const int r = i / (D / 8), ch = i % (D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int rr = blk * N + r;
+                    v = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + (int64_t)(lo + rr / G) * a.ldq +
+                                                        (int64_t)(g.h * G + rr % G) * D + ch * 8);
+                }
+                *reinterpret_cast<uint4*>(sm + L::kOffQ + (ch >> 3) * N * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
+            }
+            if (tid < N) {
+                uint64_t w = 0;
+                if (tid < rows) {
+                    const int i = (blk * N + tid) / G, T = s.nrow[g.b] / G;
+                    w = a.mask ? a.mask[lo + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+                    if (T < 64) w &= (1ull << T) - 1;
+                }
+                s.vis[tid] = w;
+                s.m[tid] = kUnseen;
+                if (tid == 0) s.bad_v = 0;
+            }
+            fence_async();
+            fence_before();
+            any_of(3, kSoftThreads, false);
+            if (lane == 0) mbar_arrive(smem_addr(&s.qfull));
+
+            float l[C];
+#pragma unroll
+            for (int i = 0; i < C; ++i) l[i] = 0.f;
+            bool stop = false;
+            for (int t = 0; t < n; ++t) {
+                const int T = done + t, sb = T & 1, pb = T % L::kPBufs;
+                const int slot = (g.t0 + t) * kTile + srow;
+                const bool valid = slot < end && pg >= 0 && pg < c.pages;
+                if (slot < end && !valid) atomicOr(&g_attn_status, kBadPage);
+                const bool plain = __all_sync(0xffffffffu, valid && slot < len);
+                if (t + 1 < n) pg = slot + kTile < end ? trow[(slot + kTile) >> shift] : -1;
+                float x[C];
+                fail = fail || !waitw(smem_addr(&s.sfull[sb]), (T >> 1) & 1, abort);
+                fence_after();
+                tm_ld<C>(tm_s + sb * N + c0 + lanebits, x);
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s.sfree[sb]));
+                // scores times f are in units of log2; a masked one is -inf whatever
+                // the scale's sign, so where there is a mask the scale goes first
+                float f = sl;
+                if (!plain) {
+                    f = 1.f;
+                    const uint64_t bit = valid ? (slot < len ? ~0ull : 1ull << (slot - len)) : 0ull;
+#pragma unroll
+                    for (int i = 0; i < C; ++i)
+                        x[i] = (slot < len && valid) || (s.vis[c0 + i] & bit) ? x[i] * sl : -INFINITY;
+                }
+                // over the reference by more than the headroom?
+                float over = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < C; ++i) over = fmaxf(over, fmaf(x[i], f, -s.m[c0 + i]));
+                if (any_of(bar, 128, over > kHeadroom || fail)) {
+                    if (any_of(bar, 128, fail)) {
+                        if (lane == 0) give_up(abort);
+                        stop = true;
+                        break;
+                    }
+                    // new references: the columns' maxima over this tile, where they are higher
+#pragma unroll
+                    for (int i = 0; i < C; ++i) {
+                        float v = x[i] * f;
+#pragma unroll
+                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                        if (lane == 0) s.red[quad][c0 + i] = v;
+                    }
+                    any_of(bar, 128, false);
+                    // O^T so far, once every product before this tile is done
+                    if (t > 0) {
+                        const int Tp = T - 1;
+                        fail = !waitw(smem_addr(&s.pfree[Tp % L::kPBufs]), (Tp / L::kPBufs) & 1, abort);
+                        fence_after();
+                    }
+#pragma unroll
+                    for (int i0 = 0; i0 < C; i0 += 8) {
+                        float down[8];
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const int i = i0 + j, col = c0 + i;
+                            const float was = s.m[col];
+                            float now = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+                            now = fmaxf(now, was);
+                            down[j] = was == now ? 1.f : fast_exp2(was - now);
+                            l[i] *= down[j];
+                        }
+                        if (t > 0) {
+#pragma unroll
+                            for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
+                                float o[8];
+                                const uint32_t at = tm_o + blkd * N + c0 + i0 + lanebits;
+                                tm_ld8(at, o);
+                                tm_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) o[j] *= down[j];
+                                tm_st8(at, o);
+                                tm_wait_st();
+                            }
+                        }
+                    }
+                    fence_before();
+                    any_of(bar, 128, false);  // every thread has read the old references
+                    for (int col = c0 + srow; col < c0 + C; col += 128)
+                        s.m[col] = fmaxf(s.m[col], fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
+                                                         fmaxf(s.red[2][col], s.red[3][col])));
+                    any_of(bar, 128, false);
+                }
+                // weights
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    x[i] = fast_exp2(fmaf(x[i], f, -s.m[c0 + i]));
+                    l[i] += x[i];
+                }
+                if (T >= L::kPBufs)
+                    fail = fail || !waitw(smem_addr(&s.pfree[pb]), ((T / L::kPBufs) - 1) & 1, abort);
+                uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
+#pragma unroll
+                for (int i = 0; i < C; i += 8) {
+                    uint4 v;
+                    __nv_bfloat162 h0 = __floats2bfloat162_rn(x[i], x[i + 1]);
+                    __nv_bfloat162 h1 = __floats2bfloat162_rn(x[i + 2], x[i + 3]);
+                    __nv_bfloat162 h2 = __floats2bfloat162_rn(x[i + 4], x[i + 5]);
+                    __nv_bfloat162 h3 = __floats2bfloat162_rn(x[i + 6], x[i + 7]);
+                    v.x = *reinterpret_cast<uint32_t*>(&h0);
+                    v.y = *reinterpret_cast<uint32_t*>(&h1);
+                    v.z = *reinterpret_cast<uint32_t*>(&h2);
+                    v.w = *reinterpret_cast<uint32_t*>(&h3);
+                    *reinterpret_cast<uint4*>(prow + ((c0 + i) >> 3) * (kTile * 16)) = v;
+                }
+                if (!plain) {
+                    // V rows that are nobody's slot: zero; of drafted slots: their non-finite values
+                    for (int e = 0; e < L::kPer; ++e) {
+                        const int q = idx + pos_v(t, n) * L::kPer + e, ent = q % L::kRing;
+                        fail = fail || !waitw(smem_addr(&s.full[ent]), (q / L::kRing) & 1, abort);
+                        if (slot < len && valid) continue;
+                        bool bad = false;
+                        for (int xa = L::kAtoms == 2 ? wg : 0; xa < (L::kAtoms == 2 ? wg + 1 : 1 - wg); ++xa) {
+                            uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + xa * kTile * 128 + srow * 128);
+                            for (int k = 0; k < 8; ++k) {
+                                if (!valid) {
+                                    v4[k] = make_uint4(0, 0, 0, 0);
+                                    continue;
+                                }
+                                uint4 v = v4[k];
+                                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
+                                bool hit = false;
+#pragma unroll
+                                for (int z = 0; z < 4; ++z) {
+                                    if ((w[z] & 0x7F80u) == 0x7F80u) {
+                                        w[z] &= 0xFFFF0000u;
+                                        hit = true;
+                                    }
+                                    if ((w[z] & 0x7F800000u) == 0x7F800000u) {
+                                        w[z] &= 0x0000FFFFu;
+                                        hit = true;
+                                    }
+                                }
+                                if (hit) v4[k] = v;
+                                bad |= hit;
+                            }
+                        }
+                        if (bad) atomicOr(&s.bad_v, 1ull << (slot - len));
+                    }
+                }
+                fence_async();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s.pfull[pb]));
+            }
+            // the columns' sums
+            if (!stop) {
+#pragma unroll
+                for (int i = 0; i < C; ++i) {
+                    float v = l[i];
+#pragma unroll
+                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+                    if (lane == 0) s.red[quad][c0 + i] = v;
+                }
+                fail = fail || !waitw(smem_addr(&s.ofull), seg & 1, abort);
+                fence_after();
+            }
+            if (any_of(3, kSoftThreads, fail || stop)) {
+                fail = true;
+                break;
+            }
+            if (tid < N) s.l[tid] = (s.red[0][tid] + s.red[1][tid]) + (s.red[2][tid] + s.red[3][tid]);
+            any_of(3, kSoftThreads, false);
+            // O^T: this thread's value row(s), its half of the columns
+            const bool whole = g.t0 == 0 && g.t1 == s.tiles[g.b];
+            const int pslot = g.first <= u0 ? 0 : 1;
+            const int64_t part = (int64_t)blockIdx.x * 2 + pslot;
+            const uint64_t badv = s.bad_v;
+#pragma unroll 1
+            for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
+                const int d = blkd * 128 + srow;
+#pragma unroll 1
+                for (int i0 = 0; i0 < C; i0 += 8) {
+                    float o[8];
+                    tm_ld8(tm_o + blkd * N + c0 + i0 + lanebits, o);
+                    tm_wait_ld();
+                    if (d >= D) continue;
+                    if (badv) {
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            for (uint64_t w = badv & s.vis[c0 + i0 + j]; w; w &= w - 1) {
+                                const int sl2 = len + __ffsll(w) - 1;
+                                const int pgv = trow[sl2 >> shift];
+                                const float v = __bfloat162float(
+                                    ((const __nv_bfloat16*)c.v)[((((int64_t)a.layer * c.pages + pgv) * c.kv_heads + g.h) *
+                                                                     c.page_size + (sl2 & (c.page_size - 1))) * D + d]);
+                                if (!isfinite(v)) o[j] += v;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const int col = c0 + i0 + j;
+                        if (col >= rows) break;
+                        if (whole) {
+                            const int rr = blk * N + col;
+                            const float sum = s.l[col];
+                            ((__nv_bfloat16*)a.out)[(int64_t)(lo + rr / G) * a.ldo + (int64_t)(g.h * G + rr % G) * D + d] =
+                                __float2bfloat16(sum == 0.f ? 0.f : o[j] / sum);
+                        } else {
+                            p.part_o[(part * N + col) * D + d] = o[j];
+                        }
+                    }
+                }
+            }
+            fence_before();
+            if (tid < rows) {
+                const float sum = s.l[tid];
+                if (!whole) {
+                    p.part_ml[part * N + tid] = make_float2(s.m[tid], sum);
+                } else if (a.lse) {
+                    const int rr = blk * N + tid;
+                    a.lse[(int64_t)(lo + rr / G) * a.q_heads + g.h * G + rr % G] =
+                        sum == 0.f ? -INFINITY : (s.m[tid] + log2f(sum)) * 0.6931471805599453f;
+                }
+            }
+            if (!whole) {
+                // the pair's CTAs: those of the groups that hold its first to its last unit
+                const int last_u = g.first + s.tiles[g.b] - 1;
+                const int glo = (int)((((int64_t)g.first + 1) * groups - 1) / units);
+                const int ghi = (int)((((int64_t)last_u + 1) * groups - 1) / units);
+                __threadfence();
+                any_of(3, kSoftThreads, false);
+                if (tid == 0) s.last = count_in(p.counters + glo * width + blk) == (unsigned)(ghi - glo);
+                any_of(3, kSoftThreads, false);
+                if (s.last) {
+                    const int lo_slot = (int)((int64_t)units * glo / groups) >= g.first ? 0 : 1;
+                    auto slot_of = [&](int q) { return (int64_t)(q * width + blk) * 2 + (q == glo ? lo_slot : 0); };
+                    if (tid < rows) {
+                        float top = kUnseen, sum = 0.f;
+                        for (int q = glo; q <= ghi; ++q) top = fmaxf(top, __ldcg(&p.part_ml[slot_of(q) * N + tid]).x);
+                        for (int q = glo; q <= ghi; ++q) {
+                            const float2 ml = __ldcg(&p.part_ml[slot_of(q) * N + tid]);
+                            sum += ml.y * (ml.x == top ? 1.f : fast_exp2(ml.x - top));
+                        }
+                        s.m[tid] = top;
+                        s.l[tid] = sum;
+                        if (a.lse) {
+                            const int rr = blk * N + tid;
+                            a.lse[(int64_t)(lo + rr / G) * a.q_heads + g.h * G + rr % G] =
+                                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+                        }
+                    }
+                    any_of(3, kSoftThreads, false);
+                    for (int i = tid; i < rows * (D / 4); i += kSoftThreads) {
+                        const int col = i / (D / 4), d = i % (D / 4) * 4;
+                        const float top = s.m[col], sum = s.l[col];
+                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+                        for (int q = glo; q <= ghi; ++q) {
+                            const int64_t at = slot_of(q) * N + col;
+                            const float m = __ldcg(&p.part_ml[at]).x;
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
+                            const float w = m == top ? 1.f : fast_exp2(m - top);
+                            acc.x += w * v.x;
+                            acc.y += w * v.y;
+                            acc.z += w * v.z;
+                            acc.w += w * v.w;
+                        }
+                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+                        __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
+                        __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
+                        const int rr = blk * N + col;
+                        *reinterpret_cast<uint2*>((uint16_t*)a.out + (int64_t)(lo + rr / G) * a.ldo +
+                                                  (int64_t)(g.h * G + rr % G) * D + d) =
+                            make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
+                    }
+                    if (tid == 0) p.counters[glo * width + blk] = 0u;
+                }
+            }
+            any_of(3, kSoftThreads, false);  // the tables of this segment are done with
+            done += n;
+            idx += 2 * n * L::kPer;
+            ++seg;
+        }
+        if (fail && lane == 0) give_up(abort);
     }
-    if (tid == 0 && a.lse) a.lse[(int64_t)row * a.q_heads + h] = any ? top + logf(sum) : -INFINITY;
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ------------------------------------------------------------------- host
+
+// The driver's tensor-map encoder, looked up once (no link against the driver).
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+int encoder(EncodeFn* out)
+{
+    static std::atomic<EncodeFn> known{nullptr};
+    EncodeFn f = known.load();
+    if (!f) {
+        void* q = nullptr;
+        cudaDriverEntryPointQueryResult r;
+        NVFP4_CUDA_TRY(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &q, 12000, cudaEnableDefault, &r));
+        if (r != cudaDriverEntryPointSuccess || !q) return fail_cuda(cudaErrorSymbolNotFound);
+        f = (EncodeFn)q;
+        known.store(f);
+    }
+    *out = f;
+    return NVFP4_OK;
+}
+
+// One layer's pool as [pages][kv_heads][page_size][head_dim], fetched 64 values x a page (at most a tile) at a time.
+int page_map(EncodeFn encode, const nvfp4_cache& c, void* pool, int layer, CUtensorMap* map)
+{
+    const cuuint64_t row = (cuuint64_t)c.head_dim * 2, head = row * c.page_size, page = head * c.kv_heads;
+    const cuuint64_t dims[4] = {(cuuint64_t)c.head_dim, (cuuint64_t)c.page_size, (cuuint64_t)c.kv_heads,
+                                (cuuint64_t)c.pages};
+    const cuuint64_t strides[3] = {row, head, page};
+    const cuuint32_t box[4] = {64, (cuuint32_t)(c.page_size < kTile ? c.page_size : kTile), 1, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, (uint8_t*)pool + (size_t)layer * c.pages * page,
+                              dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : fail_cuda(cudaErrorInvalidValue);
+}
+
+// Query rows per block: what one lane is expected to have, at most 128.
+int block_rows(int max_nodes, int rows, int g)
+{
+    const int r = (max_nodes < rows ? max_nodes : rows) * g;
+    return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+}
+
+struct Workspace {
+    size_t o, ml, bytes;
+};
+Workspace workspace(int head_dim, int sms)
+{
+    // two partials per CTA at the widest block; the counters first
+    Workspace w;
+    w.ml = ((size_t)sms * sizeof(unsigned) + 255) / 256 * 256;
+    w.o = w.ml + (size_t)sms * 2 * 128 * sizeof(float2);
+    w.bytes = w.o + (size_t)sms * 2 * 128 * head_dim * sizeof(float);
+    return w;
+}
+
+template <int D, int N>
+int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t stream)
+{
+    using L = Plan<D, N>;
+    constexpr int kBytes = L::kOffMisc + (int)sizeof(Shared) + 1024;
+    static_assert(kBytes <= 227 * 1024, "shared memory per CTA");
+    static std::atomic<unsigned long long> ready{0};  // devices whose attribute is set
+    int dev = 0;
+    NVFP4_CUDA_TRY(cudaGetDevice(&dev));
+    if (dev >= 64) return NVFP4_ERR_ARG;
+    if (!(ready.load() >> dev & 1)) {
+        NVFP4_CUDA_TRY(cudaFuncSetAttribute(attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
+        ready.fetch_or(1ull << dev);
+    }
+    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(kAttnThreads), kBytes, stream, p, mk, mv));
+    return NVFP4_OK;
+}
+
+template <int D>
+int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t stream)
+{
+    switch (n) {
+    case 16: return launch_variant<D, 16>(p, mk, mv, sms, stream);
+    case 32: return launch_variant<D, 32>(p, mk, mv, sms, stream);
+    case 64: return launch_variant<D, 64>(p, mk, mv, sms, stream);
+    default: return launch_variant<D, 128>(p, mk, mv, sms, stream);
+    }
 }
 
 }  // namespace
@@ -114,16 +934,6 @@ int read_and_clear_attn_status(unsigned* status)
     }
     *status = v;
     return NVFP4_OK;
-}
-
-static size_t attn_workspace(int rows, int q_heads, int kv_heads, int head_dim, int sms)
-{
-    (void)rows;
-    (void)q_heads;
-    (void)kv_heads;
-    (void)head_dim;
-    (void)sms;
-    return 16;
 }
 
 int validate_attn(const nvfp4_attn_args* a)
@@ -150,16 +960,28 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     AttnParams p;
     p.c = *a->cache;
     p.a = *a;
+    p.min_tiles = 1;
     int sms = 0;
-    const int st = sm_count(&sms);
+    int st = sm_count(&sms);
     if (st != NVFP4_OK) return st;
-    if (a->workspace_bytes < attn_workspace(a->rows, a->q_heads, p.c.kv_heads, p.c.head_dim, sms))
-        return NVFP4_ERR_SCRATCH;
-    const dim3 grid((unsigned)a->q_heads, (unsigned)a->rows);
-    NVFP4_CUDA_TRY(p.c.head_dim == 64    ? launch_pdl(attn_kernel<64>, grid, dim3(128), 0, stream, p)
-                   : p.c.head_dim == 128 ? launch_pdl(attn_kernel<128>, grid, dim3(128), 0, stream, p)
-                                         : launch_pdl(attn_kernel<256>, grid, dim3(128), 0, stream, p));
-    return NVFP4_OK;
+    const Workspace w = workspace(p.c.head_dim, sms);
+    if (a->workspace_bytes < w.bytes) return NVFP4_ERR_SCRATCH;
+    uint8_t* base = (uint8_t*)a->workspace;
+    p.counters = (unsigned*)base;
+    p.part_ml = (float2*)(base + w.ml);
+    p.part_o = (float*)(base + w.o);
+    EncodeFn encode = nullptr;
+    st = encoder(&encode);
+    CUtensorMap mk, mv;
+    if (st == NVFP4_OK) st = page_map(encode, p.c, p.c.k, a->layer, &mk);
+    if (st == NVFP4_OK) st = page_map(encode, p.c, p.c.v, a->layer, &mv);
+    if (st != NVFP4_OK) return st;
+    int n = block_rows(a->max_nodes, a->rows, a->q_heads / p.c.kv_heads);
+    // every block of a lane needs a CTA, whatever the hint says
+    while (n < 128 && (a->rows * (a->q_heads / p.c.kv_heads) + n - 1) / n > sms) n *= 2;
+    return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, sms, stream)
+           : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, sms, stream)
+                                 : launch_dim<256>(n, p, mk, mv, sms, stream);
 }
 
 }  // namespace nvfp4
@@ -172,7 +994,7 @@ extern "C" int nvfp4_attn_tree_workspace(int rows, int q_heads, int kv_heads, in
     if (kv_heads < 1 || q_heads < 1 || q_heads % kv_heads || q_heads > 32 * kv_heads || kv_heads > 256 ||
         (head_dim != 64 && head_dim != 128 && head_dim != 256))
         return NVFP4_ERR_SHAPE;
-    *bytes = nvfp4::attn_workspace(rows, q_heads, kv_heads, head_dim, sm_count);
+    *bytes = nvfp4::workspace(head_dim, sm_count).bytes;
     return NVFP4_OK;
 }
 
