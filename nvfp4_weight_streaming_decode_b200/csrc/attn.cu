@@ -103,7 +103,8 @@ struct Shared {  // at kOffMisc
     int base[kMaxLanes + 1];           // first unit of each lane
     int width;                         // CTAs that share a (lane, head), one per block of query rows
     uint64_t vis[128];                 // drafted slots each column sees
-    float m[128], l[128];
+    alignas(16) float m[128];
+    float l[128];
     float red[4][128];
 };
 static_assert(sizeof(Shared) <= 8192 - 1024, "room for the tables, and for aligning the buffers");
@@ -283,6 +284,19 @@ __device__ __forceinline__ Segment segment_at(const Shared& s, int lanes, int u,
 __device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
 
+// CH scores of this thread's slot from tensor memory, scaled and masked unless
+// the whole warp's slots are seen by every row (`plain`); `all`: this slot is.
+template <int CH>
+__device__ __forceinline__ void read_scores(uint32_t at, float (&x)[CH], bool plain, bool all, uint64_t bit, float sl,
+                                            const uint64_t* vis)
+{
+    tm_ld<CH>(at, x);
+    if (!plain) {
+#pragma unroll
+        for (int i = 0; i < CH; ++i) x[i] = all || (vis[i] & bit) ? x[i] * sl : -INFINITY;
+    }
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <int D, int N>
@@ -291,7 +305,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const __grid_constant__ CUtensorMap map_v)
 {
     using L = Plan<D, N>;
-    constexpr int C = L::kCols;
+    constexpr int C = L::kCols, CH = C == 64 ? 16 : C;  // columns of a softmax thread, and those it holds at once
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Shared& s = *reinterpret_cast<Shared*>(sm + L::kOffMisc);
@@ -558,27 +572,26 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 if (slot < end && !valid) atomicOr(&g_attn_status, kBadPage);
                 const bool plain = __all_sync(0xffffffffu, valid && slot < len);
                 if (t + 1 < n) pg = slot + kTile < end ? trow[(slot + kTile) >> shift] : -1;
-                float x[C];
+                // Scores times f are in units of log2; a masked one is -inf whatever
+                // the scale's sign, so where there is a mask the scale goes first.
+                const float f = plain ? sl : 1.f;
+                const bool all = slot < len && valid;
+                const uint64_t bit = valid && slot >= len ? 1ull << (slot - len) : 0ull;
                 fail = fail || !waitw(smem_addr(&s.sfull[sb]), (T >> 1) & 1, abort);
                 fence_after();
-                tm_ld<C>(tm_s + sb * N + c0 + lanebits, x);
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s.sfree[sb]));
-                // scores times f are in units of log2; a masked one is -inf whatever
-                // the scale's sign, so where there is a mask the scale goes first
-                float f = sl;
-                if (!plain) {
-                    f = 1.f;
-                    const uint64_t bit = valid ? (slot < len ? ~0ull : 1ull << (slot - len)) : 0ull;
-#pragma unroll
-                    for (int i = 0; i < C; ++i)
-                        x[i] = (slot < len && valid) || (s.vis[c0 + i] & bit) ? x[i] * sl : -INFINITY;
-                }
                 // over the reference by more than the headroom?
+                float x[CH];
                 float over = -INFINITY;
 #pragma unroll
-                for (int i = 0; i < C; ++i) over = fmaxf(over, fmaf(x[i], f, -s.m[c0 + i]));
+                for (int i0 = 0; i0 < C; i0 += CH) {
+                    read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
+#pragma unroll
+                    for (int i = 0; i < CH; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&s.m[c0 + i0 + i]);
+                        over = fmaxf(fmaxf(over, fmaf(x[i], f, -m.x)), fmaf(x[i + 1], f, -m.y));
+                        over = fmaxf(fmaxf(over, fmaf(x[i + 2], f, -m.z)), fmaf(x[i + 3], f, -m.w));
+                    }
+                }
                 if (any_of(bar, 128, over > kHeadroom || fail)) {
                     if (any_of(bar, 128, fail)) {
                         if (lane == 0) give_up(abort);
@@ -587,11 +600,16 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     }
                     // new references: the columns' maxima over this tile, where they are higher
 #pragma unroll
-                    for (int i = 0; i < C; ++i) {
-                        float v = x[i] * f;
+                    for (int i0 = 0; i0 < C; i0 += CH) {
+                        if (C > CH)
+                            read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
 #pragma unroll
-                        for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                        if (lane == 0) s.red[quad][c0 + i] = v;
+                        for (int i = 0; i < CH; ++i) {
+                            float v = x[i] * f;
+#pragma unroll
+                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+                            if (lane == 0) s.red[quad][c0 + i0 + i] = v;
+                        }
                     }
                     any_of(bar, 128, false);
                     // O^T so far, once every product before this tile is done
@@ -633,28 +651,42 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                                          fmaxf(s.red[2][col], s.red[3][col])));
                     any_of(bar, 128, false);
                 }
-                // weights
-#pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    x[i] = fast_exp2(fmaf(x[i], f, -s.m[c0 + i]));
-                    l[i] += x[i];
-                }
                 if (T >= L::kPBufs)
                     fail = fail || !waitw(smem_addr(&s.pfree[pb]), ((T / L::kPBufs) - 1) & 1, abort);
+                // weights
                 uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
 #pragma unroll
-                for (int i = 0; i < C; i += 8) {
-                    uint4 v;
-                    __nv_bfloat162 h0 = __floats2bfloat162_rn(x[i], x[i + 1]);
-                    __nv_bfloat162 h1 = __floats2bfloat162_rn(x[i + 2], x[i + 3]);
-                    __nv_bfloat162 h2 = __floats2bfloat162_rn(x[i + 4], x[i + 5]);
-                    __nv_bfloat162 h3 = __floats2bfloat162_rn(x[i + 6], x[i + 7]);
-                    v.x = *reinterpret_cast<uint32_t*>(&h0);
-                    v.y = *reinterpret_cast<uint32_t*>(&h1);
-                    v.z = *reinterpret_cast<uint32_t*>(&h2);
-                    v.w = *reinterpret_cast<uint32_t*>(&h3);
-                    *reinterpret_cast<uint4*>(prow + ((c0 + i) >> 3) * (kTile * 16)) = v;
+                for (int i0 = 0; i0 < C; i0 += CH) {
+                    if (C > CH)
+                        read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
+#pragma unroll
+                    for (int i = 0; i < CH; i += 4) {
+                        const float4 m = *reinterpret_cast<const float4*>(&s.m[c0 + i0 + i]);
+                        x[i] = fast_exp2(fmaf(x[i], f, -m.x));
+                        x[i + 1] = fast_exp2(fmaf(x[i + 1], f, -m.y));
+                        x[i + 2] = fast_exp2(fmaf(x[i + 2], f, -m.z));
+                        x[i + 3] = fast_exp2(fmaf(x[i + 3], f, -m.w));
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) l[i0 + i + j] += x[i + j];
+                    }
+#pragma unroll
+                    for (int i = 0; i < CH; i += 8) {
+                        uint4 v;
+                        __nv_bfloat162 h0 = __floats2bfloat162_rn(x[i], x[i + 1]);
+                        __nv_bfloat162 h1 = __floats2bfloat162_rn(x[i + 2], x[i + 3]);
+                        __nv_bfloat162 h2 = __floats2bfloat162_rn(x[i + 4], x[i + 5]);
+                        __nv_bfloat162 h3 = __floats2bfloat162_rn(x[i + 6], x[i + 7]);
+                        v.x = *reinterpret_cast<uint32_t*>(&h0);
+                        v.y = *reinterpret_cast<uint32_t*>(&h1);
+                        v.z = *reinterpret_cast<uint32_t*>(&h2);
+                        v.w = *reinterpret_cast<uint32_t*>(&h3);
+                        *reinterpret_cast<uint4*>(prow + ((c0 + i0 + i) >> 3) * (kTile * 16)) = v;
+                    }
                 }
+                // the scores' buffer may be filled again
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s.sfree[sb]));
                 if (!plain) {
                     // V rows that are nobody's slot: zero; of drafted slots: their non-finite values
                     for (int e = 0; e < L::kPer; ++e) {
