@@ -59,10 +59,6 @@ namespace {
 
 constexpr unsigned kBadPage = 1u, kGaveUp = 4u;
 constexpr int kTile = 128;                 // slots per tile
-constexpr int kSoftWarps = 8;
-constexpr int kSoftThreads = kSoftWarps * 32;
-constexpr int kLoadWarp = 8, kMmaWarp = 9;
-constexpr int kAttnThreads = 320;
 constexpr int kMaxLanes = NVFP4_CACHE_MAX_LANES;
 constexpr float kHeadroom = 32.f;          // weights up to 2^32 before a rescale; their sums stay far below 2^127
 constexpr float kUnseen = -3.0e38f;        // reference of a column that has seen no slot
@@ -85,7 +81,18 @@ struct Plan {
     static constexpr int kOffP = kRing * kEntry;
     static constexpr int kOffQ = kOffP + kPBufs * kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
-    static constexpr int kCols = N / 2;                      // columns per softmax thread
+    // Softmax warps come in groups of four (32 slots each) that share the columns
+    // out; 128 columns take four groups, because a thread with 64 of them spills.
+    static constexpr int kGroups = N == 128 ? 4 : 2;
+    static constexpr int kCols = N / kGroups;                // columns per softmax thread
+    static constexpr int kSoftWarps = 4 * kGroups, kSoftThreads = 32 * kSoftWarps;
+    static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
+    static constexpr int kThreads = kSoftThreads + 128;      // the last group: loads, products, two idle warps
+    // Registers: kThreads x kLaunch at launch = softmax threads x kSoft + 128 x kRest
+    // (what one side gains the other gives up, or the gaining side would wait forever).
+    static constexpr int kLaunch = kGroups == 4 ? 96 : 168, kSoft = kGroups == 4 ? 104 : 208,
+                         kRest = kGroups == 4 ? 64 : 88;
+    static_assert(kThreads * kLaunch == kSoftThreads * kSoft + 128 * kRest && kThreads * kLaunch <= 65536, "registers");
     static constexpr int kOBlocks = D > 128 ? 2 : 1;         // 128-row blocks of O^T
     // loads and products take entries in one order, so a tile of V beside one entry of K is enough to go on
     static_assert(kRing > kPer, "V of a tile fits the ring");
@@ -142,17 +149,31 @@ __device__ __forceinline__ uint64_t desc_p(uint32_t addr)
            ((uint64_t)1 << 46);
 }
 
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate)
+// The whole warp runs the code around these, and its leader (one lane, always
+// the same) issues: operands then stay in uniform registers.  Under a branch of
+// one lane each product took 105 cycles to issue, so 32 of work.
+__device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
+                                    uint32_t accumulate)
 {
     asm volatile(
-        "{\n .reg .pred p;\n setp.ne.b32 p, %4, 0;\n"
-        " tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%5, %6, %7, %8}, p;\n}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(0u), "r"(0u), "r"(0u), "r"(0u)
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, {%6, %6, %6, %6}, p;\n}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader), "r"(0u)
         : "memory");
 }
-__device__ __forceinline__ void commit(uint32_t bar)
+__device__ __forceinline__ void commit(uint32_t leader, uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    asm volatile(
+        "{\n .reg .pred e;\n setp.ne.b32 e, %1, 0;\n"
+        " @e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n}" ::"r"(bar),
+        "r"(leader)
+        : "memory");
+}
+__device__ __forceinline__ uint32_t elect()
+{
+    uint32_t r;
+    asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}" : "=r"(r));
+    return r;
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
@@ -210,18 +231,22 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
 
 // ----------------------------------------------------------- bounded waits
 
-// One thread.
-__device__ __forceinline__ bool wait1(uint32_t bar, uint32_t parity, volatile int* abort)
+// A plain test first: a try_wait costs hundreds of cycles even when the phase is complete.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity)
 {
-    for (uint32_t it = 0; it < kPolls; ++it) {
-        if (mbar_try_wait_sleep(bar, parity, kSleepNs)) return true;
-        if (*abort) return false;
-    }
-    return false;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+        " selp.u32 %0, 1, 0, p;\n}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
 }
 // A whole warp.
 __device__ __forceinline__ bool waitw(uint32_t bar, uint32_t parity, volatile int* abort)
 {
+    if (__all_sync(0xffffffffu, mbar_test(bar, parity))) return true;
     for (uint32_t it = 0; it < kPolls; ++it) {
         if (__all_sync(0xffffffffu, mbar_try_wait_sleep(bar, parity, kSleepNs))) return true;
         if (__any_sync(0xffffffffu, *abort != 0)) return false;
@@ -300,19 +325,23 @@ __device__ __forceinline__ void read_scores(uint32_t at, float (&x)[CH], bool pl
 // ---------------------------------------------------------------- the kernel
 
 template <int D, int N>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+__global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
                 const __grid_constant__ CUtensorMap map_v)
 {
     using L = Plan<D, N>;
-    constexpr int C = L::kCols, CH = C == 64 ? 16 : C;  // columns of a softmax thread, and those it holds at once
+    // columns of a softmax thread, and those it holds at once
+    constexpr int C = L::kCols, CH = N == 128 ? 16 : C;
+    constexpr int kSoftWarps = L::kSoftWarps, kSoftThreads = L::kSoftThreads, kLoadWarp = L::kLoadWarp,
+                  kMmaWarp = L::kMmaWarp;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Shared& s = *reinterpret_cast<Shared*>(sm + L::kOffMisc);
     const uint32_t ring = smem_addr(sm), pbuf = ring + L::kOffP, qbuf = ring + L::kOffQ;
     const nvfp4_cache& c = p.c;
     const nvfp4_attn_args& a = p.a;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);  // the same in all lanes, and known to be
     const int G = a.q_heads / c.kv_heads;
     const int shift = __ffs(c.page_size) - 1;
     volatile int* abort = &s.abort;
@@ -395,6 +424,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
     const int u0 = idle ? 0 : (int)((int64_t)units * group / groups);
     const int u1 = idle ? 0 : (int)((int64_t)units * (group + 1) / groups);
 
+    if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRest));
     if (warp == kLoadWarp) {
         // ---- pages -> ring
         int idx = 0;  // entries issued so far
@@ -452,78 +482,77 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 warp_wait(smem_addr(&s.full[q % L::kRing]), (q / L::kRing) & 1);
         }
     } else if (warp == kMmaWarp) {
-        // ---- the products, issued by one thread
-        if (lane == 0) {
-            constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
-            constexpr uint32_t kIdS = kBase, kIdO = kBase | (1u << 15) | (1u << 16);
-            int idx = 0, seg = 0;
-            int done = 0;  // tiles of earlier segments
-            bool ok = true;
-            for (int u = u0; ok && u < u1;) {
-                const Segment g = segment_at(s, c.lanes, u, u1);
-                u += g.t1 - g.t0;
-                if (blk * N >= s.nrow[g.b]) continue;
-                const int n = g.t1 - g.t0;
-                ok = wait1(smem_addr(&s.qfull), seg & 1, abort);
-                fence_after();
-                for (int t = 0; ok && t <= n; ++t) {
-                    if (t < n) {  // S of tile t
-                        const int T = done + t, sb = T & 1;
-                        if (T >= 2) ok = wait1(smem_addr(&s.sfree[sb]), ((T >> 1) - 1) & 1, abort);
-                        for (int e = 0; ok && e < L::kPer; ++e) {
-                            const int q = idx + pos_k(t) * L::kPer + e, slot = q % L::kRing;
-                            ok = wait1(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
-                            if (!ok) break;
-                            fence_after();
+        // ---- the products
+        const uint32_t lead = elect();
+        constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | ((uint32_t)(N >> 3) << 17) | (8u << 24);
+        constexpr uint32_t kIdS = kBase, kIdO = kBase | (1u << 15) | (1u << 16);
+        int idx = 0, seg = 0;
+        int done = 0;  // tiles of earlier segments
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s, c.lanes, u, u1);
+            u += g.t1 - g.t0;
+            if (blk * N >= s.nrow[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
+            fence_after();
+            for (int t = 0; ok && t <= n; ++t) {
+                if (t < n) {  // S of tile t
+                    const int T = done + t, sb = T & 1;
+                    if (T >= 2) ok = waitw(smem_addr(&s.sfree[sb]), ((T >> 1) - 1) & 1, abort);
+                    for (int e = 0; ok && e < L::kPer; ++e) {
+                        const int q = idx + pos_k(t) * L::kPer + e, slot = q % L::kRing;
+                        ok = waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
+                        if (!ok) break;
+                        fence_after();
 #pragma unroll
-                            for (int x = 0; x < L::kAtoms; ++x)
+                        for (int x = 0; x < L::kAtoms; ++x)
 #pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma(tm_s + sb * N, desc_k(ring + slot * L::kEntry + x * kTile * 128 + k * 32),
-                                        desc_k(qbuf + (e * L::kAtoms + x) * N * 128 + k * 32), kIdS, (e | x | k) != 0);
-                            commit(smem_addr(&s.empty[slot]));
-                        }
-                        if (ok) commit(smem_addr(&s.sfull[sb]));
+                            for (int k = 0; k < 4; ++k)
+                                mma(lead, tm_s + sb * N, desc_k(ring + slot * L::kEntry + x * kTile * 128 + k * 32),
+                                    desc_k(qbuf + (e * L::kAtoms + x) * N * 128 + k * 32), kIdS, (e | x | k) != 0);
+                        commit(lead, smem_addr(&s.empty[slot]));
                     }
-                    if (ok && t > 0) {  // O of tile t - 1
-                        const int T = done + t - 1, pb = T % L::kPBufs;
-                        ok = wait1(smem_addr(&s.pfull[pb]), (T / L::kPBufs) & 1, abort);
-                        for (int e = 0; ok && e < L::kPer; ++e) {
-                            const int q = idx + pos_v(t - 1, n) * L::kPer + e, slot = q % L::kRing;
-                            ok = wait1(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
-                            if (!ok) break;
-                            fence_after();
+                    if (ok) commit(lead, smem_addr(&s.sfull[sb]));
+                }
+                if (ok && t > 0) {  // O of tile t - 1
+                    const int T = done + t - 1, pb = T % L::kPBufs;
+                    ok = waitw(smem_addr(&s.pfull[pb]), (T / L::kPBufs) & 1, abort);
+                    for (int e = 0; ok && e < L::kPer; ++e) {
+                        const int q = idx + pos_v(t - 1, n) * L::kPer + e, slot = q % L::kRing;
+                        ok = waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
+                        if (!ok) break;
+                        fence_after();
 #pragma unroll
-                            for (int k = 0; k < kTile / 16; ++k)
-                                // head_dim 64: both halves of the 128 rows read the one atom
-                                mma(tm_o + e * N, desc_mn(ring + slot * L::kEntry + k * 2048, L::kAtoms == 2 ? kTile * 128 : 0),
-                                    desc_p(pbuf + pb * L::kPBytes + k * 256), kIdO, t > 1 || k != 0);
-                            commit(smem_addr(&s.empty[slot]));
-                        }
-                        if (ok) {
-                            commit(smem_addr(&s.pfree[pb]));
-                            if (t == n) commit(smem_addr(&s.ofull));
-                        }
+                        for (int k = 0; k < kTile / 16; ++k)
+                            // head_dim 64: both halves of the 128 rows read the one atom
+                            mma(lead, tm_o + e * N, desc_mn(ring + slot * L::kEntry + k * 2048, L::kAtoms == 2 ? kTile * 128 : 0),
+                                desc_p(pbuf + pb * L::kPBytes + k * 256), kIdO, t > 1 || k != 0);
+                        commit(lead, smem_addr(&s.empty[slot]));
+                    }
+                    if (ok) {
+                        commit(lead, smem_addr(&s.pfree[pb]));
+                        if (t == n) commit(lead, smem_addr(&s.ofull));
                     }
                 }
-                idx += 2 * n * L::kPer;
-                done += n;
-                ++seg;
             }
-            if (!ok) {
-                give_up(abort);
-                commit(smem_addr(&s.drain));
-                for (uint32_t it = 0; it < kPolls && !mbar_try_wait_sleep(smem_addr(&s.drain), 0, kSleepNs); ++it) {
-                }
-            }
+            idx += 2 * n * L::kPer;
+            done += n;
+            ++seg;
         }
-        __syncwarp();
+        if (!ok) {
+            if (lane == 0) give_up(abort);
+            commit(lead, smem_addr(&s.drain));  // products in flight (a wait that the abort does not cut short)
+            warp_wait(smem_addr(&s.drain), 0);
+        }
     } else if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoft));
         // ---- softmax: thread = slot (and value row of O^T), half the columns
         const int wg = warp >> 2, quad = warp & 3, srow = quad * 32 + lane, c0 = wg * C;
         const uint32_t lanebits = (uint32_t)(quad * 32) << 16;
         const float sl = a.scale * 1.4426950408889634f;
         const int bar = 1 + wg;
+        constexpr int kAllBar = 5;
         int seg = 0, done = 0, idx = 0;
         bool fail = false;
         for (int u = u0; u < u1;) {
@@ -558,7 +587,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
             }
             fence_async();
             fence_before();
-            any_of(3, kSoftThreads, false);
+            any_of(kAllBar, kSoftThreads, false);
             if (lane == 0) mbar_arrive(smem_addr(&s.qfull));
 
             float l[C];
@@ -694,8 +723,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                         fail = fail || !waitw(smem_addr(&s.full[ent]), (q / L::kRing) & 1, abort);
                         if (slot < len && valid) continue;
                         bool bad = false;
-                        for (int xa = L::kAtoms == 2 ? wg : 0; xa < (L::kAtoms == 2 ? wg + 1 : 1 - wg); ++xa) {
-                            uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + xa * kTile * 128 + srow * 128);
+                        if (wg < L::kAtoms) {  // one group of warps per atom
+                            uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + wg * kTile * 128 + srow * 128);
                             for (int k = 0; k < 8; ++k) {
                                 if (!valid) {
                                     v4[k] = make_uint4(0, 0, 0, 0);
@@ -739,12 +768,12 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 fail = fail || !waitw(smem_addr(&s.ofull), seg & 1, abort);
                 fence_after();
             }
-            if (any_of(3, kSoftThreads, fail || stop)) {
+            if (any_of(kAllBar, kSoftThreads, fail || stop)) {
                 fail = true;
                 break;
             }
             if (tid < N) s.l[tid] = (s.red[0][tid] + s.red[1][tid]) + (s.red[2][tid] + s.red[3][tid]);
-            any_of(3, kSoftThreads, false);
+            any_of(kAllBar, kSoftThreads, false);
             // O^T: this thread's value row(s), its half of the columns
             const bool whole = g.t0 == 0 && g.t1 == s.tiles[g.b];
             const int pslot = g.first <= u0 ? 0 : 1;
@@ -804,9 +833,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                 const int glo = (int)((((int64_t)g.first + 1) * groups - 1) / units);
                 const int ghi = (int)((((int64_t)last_u + 1) * groups - 1) / units);
                 __threadfence();
-                any_of(3, kSoftThreads, false);
+                any_of(kAllBar, kSoftThreads, false);
                 if (tid == 0) s.last = count_in(p.counters + glo * width + blk) == (unsigned)(ghi - glo);
-                any_of(3, kSoftThreads, false);
+                any_of(kAllBar, kSoftThreads, false);
                 if (s.last) {
                     const int lo_slot = (int)((int64_t)units * glo / groups) >= g.first ? 0 : 1;
                     auto slot_of = [&](int q) { return (int64_t)(q * width + blk) * 2 + (q == glo ? lo_slot : 0); };
@@ -825,7 +854,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                                 sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
                         }
                     }
-                    any_of(3, kSoftThreads, false);
+                    any_of(kAllBar, kSoftThreads, false);
                     for (int i = tid; i < rows * (D / 4); i += kSoftThreads) {
                         const int col = i / (D / 4), d = i % (D / 4) * 4;
                         const float top = s.m[col], sum = s.l[col];
@@ -852,7 +881,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1)
                     if (tid == 0) p.counters[glo * width + blk] = 0u;
                 }
             }
-            any_of(3, kSoftThreads, false);  // the tables of this segment are done with
+            any_of(kAllBar, kSoftThreads, false);  // the tables of this segment are done with
             done += n;
             idx += 2 * n * L::kPer;
             ++seg;
@@ -938,7 +967,7 @@ int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap
         NVFP4_CUDA_TRY(cudaFuncSetAttribute(attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
         ready.fetch_or(1ull << dev);
     }
-    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(kAttnThreads), kBytes, stream, p, mk, mv));
+    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(L::kThreads), kBytes, stream, p, mk, mv));
     return NVFP4_OK;
 }
 
