@@ -10,11 +10,13 @@
 // ranks the group's beams * S * beams candidates by 64-bit scores.
 //
 // Selecting k of n values, in a slice and in the merge alike: the k-th largest
-// of the 256 threads' own maxima bounds the answer from below (k different
-// elements reach it), and few elements lie above it, so one more pass collects
-// those and each counts how many rank before it.  When ties push more than
+// of a warp's 32 thread maxima bounds the answer from below (k different
+// elements reach it); the highest of the warps' bounds leaves few
+// elements above it (some 60 for k = 8), so one more pass collects those and
+// each counts how many rank before it.  (k > 32: the k-th of all maxima.)  When ties push more than
 // kListCap elements over the bound, k rounds of a block-wide maximum decide.
 #include <cuda_runtime.h>
+#include <float.h>
 #include <stdint.h>
 
 #include "cache.cuh"
@@ -24,13 +26,19 @@ namespace nvfp4 {
 
 namespace {
 
+// 256 threads of 32 logits: steps that do not grow with the slice (bounds, sums
+// across lanes, ranking) are issue-bound, so not fewer logits a thread; and the
+// code for a thread's logits runs once, so it is kept short (hits as a bit mask,
+// their values fetched again) -- fetching instructions would cost more.
 constexpr int kBeamThreads = 256;
 constexpr int kPerThread = 32;                          // logits a thread holds
 constexpr int kSliceMax = kBeamThreads * kPerThread;    // 8192
+static_assert(kPerThread <= 32, "a bit of a word per logit");
+constexpr int kWarps = kBeamThreads / 32;
 constexpr int kListCap = 512;
 constexpr int kMaxRows = NVFP4_TOPK_MAX_ROWS;
 
-struct SlicePart {
+struct alignas(16) SlicePart {
     double sum;  // of exp(x - top)
     float top;   // -inf: the slice has nothing finite
     float unused;
@@ -52,6 +60,15 @@ struct BeamParams {
     unsigned* counters; // [groups]
 };
 
+// e^x by the exponential unit, within about 2^-22 (1 + |x| / 8) of itself; terms
+// far below the maximum, where that grows, hardly count in the sum.
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
 // An order on (value, place): the larger value first, equal ones by lower place.
 template <class T>
 __device__ __forceinline__ bool before(T a, uint32_t ia, T b, uint32_t ib)
@@ -64,53 +81,78 @@ struct ListShared {
     T top[kBeamThreads];
     T val[kListCap];
     uint32_t place[kListCap];
-    T wval[kBeamThreads / 32];
-    uint32_t wplace[kBeamThreads / 32];
+    T wval[kWarps];
+    uint32_t wplace[kWarps];
     T bound;
     int count;
 };
 
+// A warp's bound: the k-th largest (k <= 32) of its lanes' values goes to *out.
+template <class T>
+__device__ __forceinline__ void warp_kth(int k, T mine, int lane, T* out)
+{
+    int rank = 0;
+#pragma unroll
+    for (int i = 0; i < 32; ++i) {
+        const T o = __shfl_sync(0xffffffffu, mine, i);
+        rank += o > mine || (o == mine && i < lane);
+    }
+    if (rank == k - 1) *out = mine;
+}
+
 // The k best of the block's elements under `before`, to emit(rank, value,
-// place).  each(f) calls f(value, place) for the calling thread's elements,
-// which all are finite or +inf (callers leave out -inf and NaN); `mine` is the
-// thread's largest, or -inf.  Returns how many there are, at most k.
-template <class T, class Each, class Emit>
-__device__ int block_best(int k, T mine, T none, Each each, Emit emit, ListShared<T>& sh)
+// place).  above(bound, f) calls f(value, place) for the calling thread's
+// elements from `bound` up, each(f) for all; both leave out -inf and NaN.  `mine`
+// is the thread's largest element, or `none`.  For k <= 32 the callers have put
+// warp_kth of it into sh.top[warp] and zeroed sh.count before a barrier.
+// Returns how many there are, at most k.
+template <class T, class Above, class Each, class Emit>
+__device__ int block_best(int k, T mine, T none, Above above, Each each, Emit emit, ListShared<T>& sh)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    sh.top[tid] = mine;
-    if (tid == 0) {
-        sh.bound = none;
-        sh.count = 0;
+    T bound;  // none: too few threads hold elements, take all
+    if (k <= 32) {
+        bound = sh.top[0];
+#pragma unroll
+        for (int w = 1; w < kWarps; ++w) bound = sh.top[w] > bound ? sh.top[w] : bound;
+    } else {
+        __syncthreads();
+        sh.top[tid] = mine;
+        if (tid == 0) sh.bound = none;
+        __syncthreads();
+        int rank = 0;
+        for (int i = 0; i < kBeamThreads; ++i) {
+            const T o = sh.top[i];
+            rank += o > mine || (o == mine && i < tid);
+        }
+        if (rank == k - 1) sh.bound = mine;
+        __syncthreads();
+        bound = sh.bound;
     }
-    __syncthreads();
-    // this thread's place among the threads' maxima; the k-th one bounds the answer
-    int rank = 0;
-    for (int i = 0; i < kBeamThreads; ++i) {
-        const T o = sh.top[i];
-        rank += o > mine || (o == mine && i < tid);
-    }
-    if (rank == k - 1) sh.bound = mine;
-    __syncthreads();
-    const T bound = sh.bound;  // none: fewer than k threads hold elements, take all
-    each([&](T v, uint32_t place) {
-        if (v >= bound) {
+    if (mine >= bound)
+        above(bound, [&](T v, uint32_t place) {
             const int pos = atomicAdd(&sh.count, 1);
             if (pos < kListCap) {
                 sh.val[pos] = v;
                 sh.place[pos] = place;
             }
-        }
-    });
+        });
     __syncthreads();
     const int n = sh.count;
     if (n <= kListCap) {
-        for (int i = tid; i < n; i += kBeamThreads) {
-            const T v = sh.val[i];
-            const uint32_t p = sh.place[i];
+        // eight threads count for one element
+        for (int i0 = 0; i0 < n; i0 += kBeamThreads / 8) {
+            const int i = i0 + (tid >> 3);
+            const bool in = i < n;
+            const T v = in ? sh.val[i] : none;
+            const uint32_t p = in ? sh.place[i] : 0u;
             int r = 0;
-            for (int j = 0; j < n; ++j) r += before(sh.val[j], sh.place[j], v, p);
-            if (r < k) emit(r, v, p);
+#pragma unroll 4
+            for (int j = tid & 7; j < n; j += 8) r += before(sh.val[j], sh.place[j], v, p);
+            r += __shfl_xor_sync(0xffffffffu, r, 1);
+            r += __shfl_xor_sync(0xffffffffu, r, 2);
+            r += __shfl_xor_sync(0xffffffffu, r, 4);
+            if (in && (tid & 7) == 0 && r < k) emit(r, v, p);
         }
         __syncthreads();
         return n < k ? n : k;
@@ -143,7 +185,7 @@ __device__ int block_best(int k, T mine, T none, Each each, Emit emit, ListShare
         __syncthreads();
         bv = sh.wval[0];
         bp = sh.wplace[0];
-        for (int w = 1; w < kBeamThreads / 32; ++w)
+        for (int w = 1; w < kWarps; ++w)
             if (before(sh.wval[w], sh.wplace[w], bv, bp)) {
                 bv = sh.wval[w];
                 bp = sh.wplace[w];
@@ -157,15 +199,16 @@ __device__ int block_best(int k, T mine, T none, Each each, Emit emit, ListShare
     return k;
 }
 
-__global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
+__global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams p)
 {
     __shared__ union {
         ListShared<float> f;
         ListShared<double> d;
     } sh;
-    __shared__ float s_w[kBeamThreads / 32];
-    __shared__ double s_d[kBeamThreads / 32];
-    __shared__ double s_lse[kMaxRows];
+    __shared__ float s_w[kWarps];
+    __shared__ double s_d[kWarps];
+    __shared__ double s_lse[kMaxRows], s_cum[kMaxRows];
+    __shared__ bool s_over[kMaxRows];
     __shared__ int s_last;
     pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -194,48 +237,64 @@ __global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
             r[4 * i + 2] = v.z;
             r[4 * i + 3] = v.w;
         }
-        // 2. the slice's maximum and sum of exp(x - maximum): pairs in 32 bits
-        // within a thread, 64 bits across threads (the joined normaliser is
-        // then good to about 1e-8, which keeps near ties of different beams in
-        // their order)
+        // 2. each warp's maximum, its sum of exp(x - maximum) (32 bits
+        // within a thread, 64 bits from there on: the joined normaliser is then
+        // good to about 1e-7 and mostly far better, which keeps near ties of
+        // different beams in their order) and its bound for the selection
         float mine = kNone;
 #pragma unroll
         for (int i = 0; i < kPerThread; ++i) mine = fmaxf(mine, r[i]);
         float top = mine;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        if (lane == 0) s_w[warp] = top;
-        __syncthreads();
-        top = s_w[0];
-#pragma unroll
-        for (int w = 1; w < kBeamThreads / 32; ++w) top = fmaxf(top, s_w[w]);
         const float ref = top == kNone ? 0.f : top;  // nothing but -inf (or NaN, which the sum keeps)
-        float e[kPerThread];
+        float e[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) e[i] = expf(r[i] - ref);
-#pragma unroll
-        for (int w = kPerThread / 2; w > 0; w >>= 1)
-#pragma unroll
-            for (int i = 0; i < w; ++i) e[i] += e[i + w];
-        double sum = (double)e[0];
+        for (int i = 0; i < kPerThread; ++i) e[i % 4] += exp_fast(r[i] - ref);
+        double sum = (double)((e[0] + e[1]) + (e[2] + e[3]));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) s_d[warp] = sum;
+        if (lane == 0) {
+            s_w[warp] = top;
+            s_d[warp] = sum;
+        }
+        if (tid == 0) sh.f.count = 0;
+        if (p.beams <= 32) warp_kth(p.beams, mine, lane, &sh.f.top[warp]);
         __syncthreads();
-        if (tid == 0) {
-            for (int w = 1; w < kBeamThreads / 32; ++w) sum += s_d[w];
-            p.part[at].sum = sum;
-            p.part[at].top = top;
+        if (warp == kWarps - 1) {  // the slice's, from the warps'
+            const float wt = lane < kWarps ? s_w[lane] : kNone;
+            double ws = lane < kWarps ? s_d[lane] : 0.0;
+            float all = wt;
+#pragma unroll
+            for (int off = kWarps / 2; off > 0; off >>= 1) all = fmaxf(all, __shfl_xor_sync(0xffffffffu, all, off));
+            ws *= (double)(wt == all ? 1.f : expf(wt - all));
+#pragma unroll
+            for (int off = kWarps / 2; off > 0; off >>= 1) ws += __shfl_xor_sync(0xffffffffu, ws, off);
+            if (lane == 0) {
+                p.part[at].sum = ws;
+                p.part[at].top = all;
+            }
         }
         // 3. the slice's best
         float* cx = p.cand_x + at * p.beams;
         int32_t* cv = p.cand_v + at * p.beams;
         const int got = block_best<float>(
             p.beams, mine, kNone,
-            [&](auto f) {
+            [&](float bound, auto f) {
+                bound = fmaxf(bound, -FLT_MAX);  // never -inf
+                uint32_t hits = 0;
 #pragma unroll
-                for (int i = 0; i < kPerThread; ++i)
-                    if (r[i] > kNone) f(r[i], (uint32_t)(lo + 4 * tid + 4 * kBeamThreads * (i / 4) + i % 4));
+                for (int i = 0; i < kPerThread; ++i) hits |= r[i] >= bound ? 1u << i : 0u;
+                for (; hits; hits &= hits - 1) {
+                    const int i = __ffs(hits) - 1, q = 4 * tid + 4 * kBeamThreads * (i / 4) + i % 4;
+                    f(__ldg(x + q), (uint32_t)(lo + q));
+                }
+            },
+            [&](auto f) {
+                for (int q = tid; q < n; q += kBeamThreads) {
+                    const float v = __ldg(x + q);
+                    if (v > kNone) f(v, (uint32_t)(lo + q));
+                }
             },
             [&](int rank, float v, uint32_t place) {
                 cx[rank] = v;
@@ -249,60 +308,106 @@ __global__ void __launch_bounds__(kBeamThreads) beam_kernel(const BeamParams p)
     if (tid == 0) s_last = count_in(p.counters + g) == (unsigned)(p.beams * p.S - 1);
     __syncthreads();
     if (!s_last) return;
-    for (int w = warp; w < p.beams; w += kBeamThreads / 32) {
-        const long long row = (long long)(g * p.beams + w) * p.S;
-        const bool over = p.finished && p.finished[g * p.beams + w] != 0;
-        double top = -INFINITY;
-        if (!over)
-            for (int i = lane; i < p.S; i += 32) top = fmax(top, (double)__ldcg(&p.part[row + i].top));
+    // Candidate i of the group is place q = i % per of row w = i / per.  Up to
+    // kHeld per thread are fetched at once, before the normalisers they need.
+    const int per = p.S * p.beams, n = p.beams * per;
+    constexpr int kHeld = 8;
+    const bool held = n <= kHeld * kBeamThreads;
+    float hx[kHeld];
+    int hv[kHeld];
+    const long long cells = (long long)g * p.beams * per;
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) top = fmax(top, __shfl_xor_sync(0xffffffffu, top, off));
-        double sum = 0.0;
-        if (!over)
-            for (int i = lane; i < p.S; i += 32)
-                sum += __ldcg(&p.part[row + i].sum) * exp((double)__ldcg(&p.part[row + i].top) - top);
+    for (int j = 0; j < kHeld; ++j) {
+        const int i = tid + j * kBeamThreads;
+        hv[j] = -1;
+        if (held && i < n) {
+            hv[j] = __ldcg(p.cand_v + cells + i);
+            hx[j] = __ldcg(p.cand_x + cells + i);
+        }
+    }
+    if (tid == 0) sh.d.count = 0;
+    for (int w = warp; w < p.beams; w += kWarps) {
+        const int row = g * p.beams + w;
+        const bool over = p.finished && p.finished[row] != 0;
+        double norm = 0.0;
+        if (!over) {
+            // joined in lane order, two slices a lane held, any further ones in turn
+            const float4* part = reinterpret_cast<const float4*>(p.part + (long long)row * p.S);
+            const float4 none4 = make_float4(0.f, 0.f, kNone, 0.f);
+            const float4 q0 = lane < p.S ? __ldcg(part + lane) : none4;
+            const float4 q1 = lane + 32 < p.S ? __ldcg(part + lane + 32) : none4;
+            float top = fmaxf(q0.z, q1.z);
+            for (int i = lane + 64; i < p.S; i += 32) top = fmaxf(top, __ldcg(part + i).z);
 #pragma unroll
-        for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-        if (lane == 0) s_lse[w] = top + log(sum);
+            for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+            auto term = [&](const float4& q) {
+                return __hiloint2double(__float_as_int(q.y), __float_as_int(q.x)) * (double)expf(q.z - top);
+            };
+            double sum = lane < p.S ? term(q0) : 0.0;
+            if (lane + 32 < p.S) sum += term(q1);
+            for (int i = lane + 64; i < p.S; i += 32) sum += term(__ldcg(part + i));
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+            norm = (double)top + log(sum);
+        }
+        if (lane == 0) {
+            s_lse[w] = norm;
+            s_cum[w] = (double)p.scores[row];
+            s_over[w] = over;
+        }
     }
     __syncthreads();
-    const int per = p.S * p.beams, n = p.beams * per;
     const double dnone = -INFINITY;
-    // candidate i of the group: its 64-bit score (none: not one) and w * V + v
-    auto cand = [&](int i, double& key, uint32_t& place) {
-        const int w = i / per, q = i - w * per, row = g * p.beams + w;
-        const double cum = (double)p.scores[row];
-        key = dnone;
-        if (p.finished && p.finished[row] != 0) {
-            place = (uint32_t)w * (uint32_t)p.V + (uint32_t)p.eos;
-            if (q == 0) key = cum;
-        } else {
-            const int v = __ldcg(p.cand_v + (long long)row * per + q);
-            place = (uint32_t)w * (uint32_t)p.V + (uint32_t)(v < 0 ? 0 : v);
-            if (v >= 0) key = cum + ((double)__ldcg(p.cand_x + (long long)row * per + q) - s_lse[w]);
-        }
-        if (!(key > dnone)) key = dnone;  // NaN too
+    // its 64-bit score (none: not a candidate) and w * V + v
+    auto cand = [&](int i, float x, int v, double& key, uint32_t& place) {
+        const int w = i / per;
+        const bool over = s_over[w];
+        if (over) v = i == w * per ? p.eos : -1;
+        place = (uint32_t)w * (uint32_t)p.V + (uint32_t)(v < 0 ? 0 : v);
+        key = over ? s_cum[w] : s_cum[w] + ((double)x - s_lse[w]);
+        if (v < 0 || !(key > dnone)) key = dnone;  // NaN too
     };
+    double hk[kHeld];
+    uint32_t hp[kHeld];
     double mine = dnone;
-    for (int i = tid; i < n; i += kBeamThreads) {
-        double key;
-        uint32_t place;
-        cand(i, key, place);
-        mine = fmax(mine, key);
+    if (held) {
+#pragma unroll
+        for (int j = 0; j < kHeld; ++j) {
+            hk[j] = dnone;
+            hp[j] = 0u;
+            const int i = tid + j * kBeamThreads;
+            if (i < n) cand(i, hx[j], hv[j], hk[j], hp[j]);
+            mine = fmax(mine, hk[j]);
+        }
     }
+    auto each_cand = [&](auto f) {
+        if (held) {
+#pragma unroll
+            for (int j = 0; j < kHeld; ++j)
+                if (hk[j] > dnone) f(hk[j], hp[j]);
+        } else {
+            for (int i = tid; i < n; i += kBeamThreads) {
+                double key;
+                uint32_t place;
+                cand(i, __ldcg(p.cand_x + cells + i), __ldcg(p.cand_v + cells + i), key, place);
+                if (key > dnone) f(key, place);
+            }
+        }
+    };
+    if (!held) each_cand([&](double key, uint32_t) { mine = fmax(mine, key); });
+    if (p.beams <= 32) warp_kth(p.beams, mine, lane, &sh.d.top[warp]);
+    __syncthreads();
     const int o = g * p.beams;
     __shared__ float o_score[kMaxRows];
     __shared__ int o_parent[kMaxRows], o_token[kMaxRows], o_done[kMaxRows];
     const int got = block_best<double>(
         p.beams, mine, dnone,
-        [&](auto f) {
-            for (int i = tid; i < n; i += kBeamThreads) {
-                double key;
-                uint32_t place;
-                cand(i, key, place);
-                if (key > dnone) f(key, place);
-            }
+        [&](double bound, auto f) {
+            each_cand([&](double key, uint32_t place) {
+                if (key >= bound) f(key, place);
+            });
         },
+        each_cand,
         [&](int rank, double key, uint32_t place) {
             const int w = (int)(place / (uint32_t)p.V), v = (int)(place - (uint32_t)w * (uint32_t)p.V);
             o_score[rank] = (float)key;
