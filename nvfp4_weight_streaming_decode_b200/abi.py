@@ -13,6 +13,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # NVFP4_LIB may name another build of the same library (same ABI).
@@ -70,6 +71,12 @@ class Nvfp4AttnArgs(ctypes.Structure):
                 ("workspace_bytes", ctypes.c_uint64)]
 
 
+# The two argument structs as one native-layout record each: filling a ctypes
+# structure field by field costs microseconds that a decode step would feel.
+_ROPE_ARGS = struct.Struct("@P6iPqPPqPPPq")
+_ATTN_ARGS = struct.Struct("@P4ifiPqPPPqPPQ")
+
+
 class Nvfp4Expert(ctypes.Structure):
     _fields_ = [("wq", _P), ("ws", _P), ("gscale", _F), ("reserved", ctypes.c_int32)]
 
@@ -97,8 +104,8 @@ _SIGNATURES = {
     "nvfp4_cache_reserve": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P, _P]),
     "nvfp4_cache_compact": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P, _I, _P]),
     "nvfp4_cache_trim": (_I, [ctypes.POINTER(Nvfp4Cache), _P, _P]),
-    "nvfp4_rope_append": (_I, [ctypes.POINTER(Nvfp4RopeArgs), _P]),
-    "nvfp4_attn_tree": (_I, [ctypes.POINTER(Nvfp4AttnArgs), _P]),
+    "nvfp4_rope_append": (_I, [_P, _P]),
+    "nvfp4_attn_tree": (_I, [_P, _P]),
     "nvfp4_attn_tree_workspace": (_I, [_I, _I, _I, _I, _I, ctypes.POINTER(_SZ)]),
     "nvfp4_beam_select": (_I, [_P, _I, _I, _I64, _I64, _P, _P, _I, _P, _P, _P, _P, _P, _SZ, _P]),
     "nvfp4_beam_select_workspace": (_I, [_I, _I, _I64, _I, ctypes.POINTER(_SZ)]),
@@ -251,10 +258,12 @@ def nvfp4_cache_trim(cache, new_len, stream):
 
 
 def nvfp4_rope_append(args, stream):
+    """args: an Nvfp4RopeArgs by reference (ctypes.byref)."""
     return load().nvfp4_rope_append(args, _s(stream))
 
 
 def nvfp4_attn_tree(args, stream):
+    """args: an Nvfp4AttnArgs by reference (ctypes.byref)."""
     return load().nvfp4_attn_tree(args, _s(stream))
 
 
@@ -426,8 +435,7 @@ def _want(t, name, dtype, device, shape=None):
     """Raise unless `t` is a contiguous tensor of this dtype, device and shape; its pointer (None for None)."""
     if t is None:
         return None
-    if t.dtype != dtype or t.device != device or not t.is_contiguous() or (shape is not None and
-                                                                           tuple(t.shape) != shape):
+    if t.dtype is not dtype or t.device != device or not t.is_contiguous() or (shape is not None and t.shape != shape):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor" + (f" of shape {shape}" if shape else "") +
                          f" on {device}: got {t.dtype} {tuple(t.shape)} on {t.device}")
     return t.data_ptr()
@@ -435,13 +443,13 @@ def _want(t, name, dtype, device, shape=None):
 
 def _heads(t, name, dtype, device, heads, dim):
     """Check a [rows][heads][dim] or [rows][heads * dim] tensor whose rows are contiguous; (rows, row stride, pointer)."""
-    if t.dtype != dtype or t.device != device:
+    if t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be a {dtype} tensor on {device}: got {t.dtype} on {t.device}")
     shape, stride = t.shape, t.stride()
-    flat = len(shape) == 2 and shape[1] == heads * dim and stride[1] == 1
-    deep = (len(shape) == 3 and shape[1] == heads and shape[2] == dim and stride[2] == 1 and
-            (stride[1] == dim or heads == 1))
-    if not (flat or deep):
+    n = len(shape)
+    if not ((n == 2 and shape[1] == heads * dim and stride[1] == 1) or
+            (n == 3 and shape[1] == heads and shape[2] == dim and stride[2] == 1 and
+             (stride[1] == dim or heads == 1))):
         raise ValueError(f"{name} must be [rows][{heads}][{dim}] with contiguous rows: got {tuple(shape)} with "
                          f"strides {stride}")
     # a single row has no next one: its stride may be anything
@@ -451,24 +459,34 @@ def _heads(t, name, dtype, device, heads, dim):
 class _on_device:
     """Make `device` current for a call and give the stream it goes to: the device's current one, or the caller's."""
 
+    __slots__ = ("index", "back", "ptr")
+
     def __init__(self, device, stream=None):
-        import torch
         if stream is not None and stream.device != device:
             raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.index, self.back, self.cuda = device.index, None, torch.cuda
-        self.ptr = (torch.cuda.current_stream(device) if stream is None else stream).cuda_stream
+        self.index, self.back = device.index, None
+        self.ptr = _current_stream(device.index) if stream is None else stream.cuda_stream
 
     def __enter__(self):
-        now = self.cuda.current_device()
+        import torch
+        now = torch.cuda.current_device()
         if now != self.index:
             self.back = now
-            self.cuda.set_device(self.index)
+            torch.cuda.set_device(self.index)
         return self.ptr
 
     def __exit__(self, *exc):
         if self.back is not None:
-            self.cuda.set_device(self.back)
+            import torch
+            torch.cuda.set_device(self.back)
         return False
+
+
+def _current_stream(index):
+    """The current stream's handle on a device; without building a Stream object where torch allows (1.5 us a call)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(index) if raw is not None else torch.cuda.current_stream(index).cuda_stream
 
 
 class Cache:
@@ -499,6 +517,7 @@ class Cache:
         self.scratch = torch.zeros(4 * lanes + 4, dtype=i32, device=dev)
         self.c = Nvfp4Cache(kp, vp, tp, lp, rp, self.scratch.data_ptr(), layers, pages, heads, page, dim, lanes, width, 0)
         self._ref = ctypes.byref(self.c)
+        self._at = ctypes.addressof(self.c)
 
     @classmethod
     def empty(cls, layers, pages, kv_heads, page_size, head_dim, lanes, max_pages, device):
@@ -551,9 +570,8 @@ class Cache:
             check(load().nvfp4_cache_trim(self._ref, np_, s), "nvfp4_cache_trim")
 
 
-def rope_args(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, style=NVFP4_ROPE_HALVES, row_start=None,
-              q=None):
-    """(Nvfp4RopeArgs, q) of a rotary append; see rope_append."""
+def _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q):
+    """(nvfp4_rope_args as bytes, q) of a rotary append; see rope_append."""
     import torch
     dev, dim = cache.device, cache.head_dim
     rows, ldy, yp = _heads(y, "y", torch.float32, dev, q_heads + 2 * cache.kv_heads, dim)
@@ -562,18 +580,18 @@ def rope_args(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, sty
     qrows, ldq, qp = _heads(q, "q", torch.bfloat16, dev, q_heads, dim)
     if qrows != rows:
         raise ValueError(f"q has {qrows} rows, y {rows}")
-    half = 0 if inv_freq is None else inv_freq.numel()
-    axes, ldp, pp = 1, rows, None
-    if half:
+    half, axes, pp, fp = 0, 1, None, None
+    if inv_freq is not None:
+        half = inv_freq.shape[0]
         pp = _want(positions, "positions", torch.int32, dev)
         if positions is None or positions.dim() > 2 or positions.shape[-1] != rows:
             raise ValueError(f"positions must be [{rows}] or [axes][{rows}]")
         axes = 1 if positions.dim() == 1 else positions.shape[0]
+        fp = _want(inv_freq, "inv_freq", torch.float64, dev, (half,))
     sp = _want(row_start, "row_start", torch.int32, dev, (cache.lanes + 1,))
     ap = _want(pair_axis, "pair_axis", torch.uint8, dev, (half,))
-    fp = _want(inv_freq, "inv_freq", torch.float64, dev, (half,)) if half else None
-    return Nvfp4RopeArgs(ctypes.pointer(cache.c), layer, rows, q_heads, 2 * half, style, axes, yp, ldy, sp, pp, ldp, ap,
-                         fp, qp, ldq), q
+    return _ROPE_ARGS.pack(cache._at, layer, rows, q_heads, 2 * half, style, axes, yp, ldy, sp or 0, pp or 0, rows,
+                           ap or 0, fp or 0, qp, ldq), q
 
 
 def rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, style=NVFP4_ROPE_HALVES,
@@ -587,9 +605,9 @@ def rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, s
         import torch
         with torch.cuda.stream(stream):
             return rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
-    a, q = rope_args(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
+    a, q = _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
     with _on_device(cache.device) as s:
-        check(load().nvfp4_rope_append(ctypes.byref(a), s), "nvfp4_rope_append")
+        check(load().nvfp4_rope_append(a, s), "nvfp4_rope_append")
     return q
 
 
@@ -611,9 +629,8 @@ def attn_tree_workspace(cache, rows, q_heads):
     return torch.zeros(n, dtype=torch.uint8, device=cache.device)
 
 
-def attn_args(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, out=None, want_lse=False, lse=None,
-              workspace=None):
-    """(Nvfp4AttnArgs, out, lse, workspace) of an attention call; see attn_tree."""
+def _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace):
+    """(nvfp4_attn_args as bytes, out, lse, workspace) of an attention call; see attn_tree."""
     import torch
     dev, dim = cache.device, cache.head_dim
     heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // dim
@@ -631,8 +648,8 @@ def attn_args(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, ou
     if workspace is None:
         workspace = attn_tree_workspace(cache, rows, heads)
     wp = _want(workspace, "workspace", torch.uint8, dev)
-    return Nvfp4AttnArgs(ctypes.pointer(cache.c), layer, rows, heads, max_nodes, scale, 0, qp, ldq, sp, mp, op, ldo, ep,
-                         wp, workspace.numel()), out, lse, workspace
+    return _ATTN_ARGS.pack(cache._at, layer, rows, heads, max_nodes, scale, 0, qp, ldq, sp or 0, mp or 0, op, ldo,
+                           ep or 0, wp, workspace.shape[0]), out, lse, workspace
 
 
 def attn_tree(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, out=None, want_lse=False, lse=None,
@@ -647,9 +664,10 @@ def attn_tree(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, ou
         import torch
         with torch.cuda.stream(stream):
             return attn_tree(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
-    a, out, lse, workspace = attn_args(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
+    a, out, lse, workspace = _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse,
+                                          workspace)
     with _on_device(cache.device) as s:
-        check(load().nvfp4_attn_tree(ctypes.byref(a), s), "nvfp4_attn_tree")
+        check(load().nvfp4_attn_tree(a, s), "nvfp4_attn_tree")
     return out if lse is None else (out, lse)
 
 
@@ -676,13 +694,15 @@ def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=No
     if dev.type != "cuda":
         raise ValueError(f"logits must be in device memory: got {dev}")
     groups, beams = scores.shape
-    if logits.dim() != 2 or logits.shape[0] != groups * beams or logits.dtype != torch.float32 or \
-            (logits.shape[1] > 1 and logits.stride(1) != 1):
+    size = logits.shape
+    if len(size) != 2 or size[0] != groups * beams or logits.dtype is not torch.float32 or \
+            (size[1] > 1 and logits.stride(1) != 1):
         raise ValueError(f"logits must be float32 [{groups * beams}][vocab] with contiguous rows")
-    V = logits.shape[1] if vocab is None else int(vocab)
-    if V > logits.shape[1]:
-        raise ValueError(f"vocab {V} is past the logits' {logits.shape[1]} columns")
-    ldv = logits.stride(0) if groups * beams > 1 else (max(logits.stride(0), V) + 3) // 4 * 4
+    V = size[1] if vocab is None else int(vocab)
+    if V > size[1]:
+        raise ValueError(f"vocab {V} is past the logits' {size[1]} columns")
+    # a single row has no next one: its stride may be anything
+    ldv = logits.stride(0) if size[0] > 1 else (V + 3) // 4 * 4
     f32, i32, u8 = torch.float32, torch.int32, torch.uint8
     shape = (groups, beams)
     if scores_out is None:
@@ -701,7 +721,7 @@ def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=No
            _want(workspace, "workspace", u8, dev))
     with _on_device(dev) as s:
         check(load().nvfp4_beam_select(logits.data_ptr(), groups, beams, V, ldv, ptr[0], ptr[1], eos, ptr[2], ptr[3],
-                                       ptr[4], ptr[5], ptr[6], workspace.numel(), s), "nvfp4_beam_select")
+                                       ptr[4], ptr[5], ptr[6], workspace.shape[0], s), "nvfp4_beam_select")
     return scores_out, parent, token, finished_out
 
 

@@ -160,6 +160,17 @@ def test_struct_layouts_match_the_header(tmp_path):
                    abi.Nvfp4AttnArgs.workspace_bytes.offset]
 
 
+def test_packed_records_have_the_structs_layout():
+    """The bytes the helpers pass are the ctypes structures field by field."""
+    r = abi.Nvfp4RopeArgs.from_buffer_copy(abi._ROPE_ARGS.pack(*range(1, 17)))
+    assert ctypes.sizeof(r) == abi._ROPE_ARGS.size and ctypes.addressof(r.cache.contents) == 1
+    names = [n for n, _ in r._fields_][1:]
+    assert [getattr(r, n) for n in names] == list(range(2, 17))
+    a = abi.Nvfp4AttnArgs.from_buffer_copy(abi._ATTN_ARGS.pack(*range(1, 17)))
+    assert ctypes.sizeof(a) == abi._ATTN_ARGS.size and ctypes.addressof(a.cache.contents) == 1
+    assert [getattr(a, n) for n in [n for n, _ in a._fields_][1:]] == list(range(2, 17))
+
+
 def test_helpers_refuse_host_tensors():
     import torch
     k = torch.zeros((1, 2, 1, 16, 64), dtype=torch.bfloat16)
