@@ -456,30 +456,25 @@ def _heads(t, name, dtype, device, heads, dim):
     return shape[0], (stride[0] if shape[0] > 1 else heads * dim), t.data_ptr()
 
 
-class _on_device:
-    """Make `device` current for a call and give the stream it goes to: the device's current one, or the caller's."""
-
-    __slots__ = ("index", "back", "ptr")
-
-    def __init__(self, device, stream=None):
-        if stream is not None and stream.device != device:
-            raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
-        self.index, self.back = device.index, None
-        self.ptr = _current_stream(device.index) if stream is None else stream.cuda_stream
-
-    def __enter__(self):
-        import torch
-        now = torch.cuda.current_device()
-        if now != self.index:
-            self.back = now
-            torch.cuda.set_device(self.index)
-        return self.ptr
-
-    def __exit__(self, *exc):
-        if self.back is not None:
-            import torch
-            torch.cuda.set_device(self.back)
-        return False
+def _call(name, device, stream, *args):
+    """The library's `name` with these arguments and a stream -- the device's current one, or the caller's -- with the
+    device current; raises what its status says."""
+    import torch
+    index = device.index
+    if stream is None:
+        ptr = _current_stream(index)
+    elif stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
+    else:
+        ptr = stream.cuda_stream
+    fn = getattr(load(), name)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, ptr)
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, ptr)
+    if st != NVFP4_OK:
+        check(st, name)
 
 
 def _current_stream(index):
@@ -540,16 +535,14 @@ class Cache:
     def fork(self, parent, stream=None):
         """Lane i takes lane parent[i]'s pages and length (-1: emptied)."""
         pp = self._lanes(parent, "parent")
-        with _on_device(self.device, stream) as s:
-            check(load().nvfp4_cache_fork(self._ref, pp, s), "nvfp4_cache_fork")
+        _call("nvfp4_cache_fork", self.device, stream, self._ref, pp)
 
     def reserve(self, want, ok=None, stream=None):
         """Room for want[b] more slots in each lane; shared last pages are copied.
         ok: int32 [1], set to 0 if the pool had too few free pages."""
         import torch
         wp, op = self._lanes(want, "want"), _want(ok, "ok", torch.int32, self.device, (1,))
-        with _on_device(self.device, stream) as s:
-            check(load().nvfp4_cache_reserve(self._ref, wp, op, s), "nvfp4_cache_reserve")
+        _call("nvfp4_cache_reserve", self.device, stream, self._ref, wp, op)
 
     def compact(self, count, path=None, stream=None):
         """Commit count[b] drafted slots of each lane, those numbered path[b][:count[b]] (None: the first ones)."""
@@ -560,14 +553,12 @@ class Cache:
             if path.dim() != 2 or path.shape[0] != self.lanes:
                 raise ValueError(f"path must be [{self.lanes}][n]: got {tuple(path.shape)}")
             ld = path.shape[1]
-        with _on_device(self.device, stream) as s:
-            check(load().nvfp4_cache_compact(self._ref, cp, pp, ld, s), "nvfp4_cache_compact")
+        _call("nvfp4_cache_compact", self.device, stream, self._ref, cp, pp, ld)
 
     def trim(self, new_len, stream=None):
         """Cut lanes back to new_len[b] slots."""
         np_ = self._lanes(new_len, "new_len")
-        with _on_device(self.device, stream) as s:
-            check(load().nvfp4_cache_trim(self._ref, np_, s), "nvfp4_cache_trim")
+        _call("nvfp4_cache_trim", self.device, stream, self._ref, np_)
 
 
 def _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q):
@@ -606,8 +597,7 @@ def rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, s
         with torch.cuda.stream(stream):
             return rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
     a, q = _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
-    with _on_device(cache.device) as s:
-        check(load().nvfp4_rope_append(a, s), "nvfp4_rope_append")
+    _call("nvfp4_rope_append", cache.device, None, a)
     return q
 
 
@@ -636,12 +626,14 @@ def _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_l
     heads = q.shape[1] if q.dim() == 3 else q.shape[-1] // dim
     rows, ldq, qp = _heads(q, "q", torch.bfloat16, dev, heads, dim)
     if out is None:
-        out = torch.empty((rows, heads, dim), dtype=torch.bfloat16, device=dev)
-    orows, ldo, op = _heads(out, "out", torch.bfloat16, dev, heads, dim)
-    if orows != rows:
-        raise ValueError(f"out has {orows} rows, q {rows}")
+        out = torch.empty_strided((rows, heads, dim), (heads * dim, dim, 1), dtype=torch.bfloat16, device=dev)
+        ldo, op = heads * dim, out.data_ptr()
+    else:
+        orows, ldo, op = _heads(out, "out", torch.bfloat16, dev, heads, dim)
+        if orows != rows:
+            raise ValueError(f"out has {orows} rows, q {rows}")
     if lse is None and want_lse:
-        lse = torch.empty((rows, heads), dtype=torch.float32, device=dev)
+        lse = torch.empty_strided((rows, heads), (heads, 1), dtype=torch.float32, device=dev)
     sp = _want(row_start, "row_start", torch.int32, dev, (cache.lanes + 1,))
     mp = _want(mask, "mask", torch.int64, dev, (rows,))
     ep = _want(lse, "lse", torch.float32, dev, (rows, heads))
@@ -666,8 +658,7 @@ def attn_tree(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, ou
             return attn_tree(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
     a, out, lse, workspace = _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse,
                                           workspace)
-    with _on_device(cache.device) as s:
-        check(load().nvfp4_attn_tree(a, s), "nvfp4_attn_tree")
+    _call("nvfp4_attn_tree", cache.device, None, a)
     return out if lse is None else (out, lse)
 
 
@@ -705,23 +696,22 @@ def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=No
     ldv = logits.stride(0) if size[0] > 1 else (V + 3) // 4 * 4
     f32, i32, u8 = torch.float32, torch.int32, torch.uint8
     shape = (groups, beams)
+    sp = _want(scores, "scores", f32, dev, shape)
     if scores_out is None:
-        scores_out = torch.empty(shape, dtype=f32, device=dev)
+        scores_out = torch.empty_like(scores)
     if parent is None:
-        parent = torch.empty(shape, dtype=i32, device=dev)
+        parent = torch.empty_like(scores, dtype=i32)
     if token is None:
-        token = torch.empty(shape, dtype=i32, device=dev)
+        token = torch.empty_like(scores, dtype=i32)
     if finished_out is None:
-        finished_out = torch.empty(shape, dtype=u8, device=dev)
+        finished_out = torch.empty_like(scores, dtype=u8)
     if workspace is None:
         workspace = beam_select_workspace(groups, beams, V, dev)
-    ptr = (_want(scores, "scores", f32, dev, shape), _want(finished, "finished", u8, dev, shape),
-           _want(scores_out, "scores_out", f32, dev, shape), _want(parent, "parent", i32, dev, shape),
-           _want(token, "token", i32, dev, shape), _want(finished_out, "finished_out", u8, dev, shape),
-           _want(workspace, "workspace", u8, dev))
-    with _on_device(dev) as s:
-        check(load().nvfp4_beam_select(logits.data_ptr(), groups, beams, V, ldv, ptr[0], ptr[1], eos, ptr[2], ptr[3],
-                                       ptr[4], ptr[5], ptr[6], workspace.shape[0], s), "nvfp4_beam_select")
+    _call("nvfp4_beam_select", dev, None, logits.data_ptr(), groups, beams, V, ldv, sp,
+          _want(finished, "finished", u8, dev, shape), eos, _want(scores_out, "scores_out", f32, dev, shape),
+          _want(parent, "parent", i32, dev, shape), _want(token, "token", i32, dev, shape),
+          _want(finished_out, "finished_out", u8, dev, shape), _want(workspace, "workspace", u8, dev),
+          workspace.shape[0])
     return scores_out, parent, token, finished_out
 
 
