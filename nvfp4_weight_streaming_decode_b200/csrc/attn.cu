@@ -87,7 +87,7 @@ struct Plan {
     static constexpr int kCols = N / kGroups;                // columns per softmax thread
     static constexpr int kSoftWarps = 4 * kGroups, kSoftThreads = 32 * kSoftWarps;
     static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
-    static constexpr int kThreads = kSoftThreads + 128;      // the last group: loads, products, two idle warps
+    static constexpr int kThreads = kSoftThreads + 128;      // the last group: pages, products, queries, an idle warp
     // Registers: kThreads x kLaunch at launch = softmax threads x kSoft + 128 x kRest
     // (what one side gains the other gives up, or the gaining side would wait forever).
     static constexpr int kLaunch = kGroups == 4 ? 96 : 168, kSoft = kGroups == 4 ? 104 : 208,
@@ -101,20 +101,22 @@ struct Plan {
 
 struct Shared {  // at kOffMisc
     uint64_t full[12], empty[12];
-    uint64_t sfull[2], sfree[2], pfull[2], pfree[2];
-    uint64_t qfull, ofull, drain;
+    uint64_t sfull[2], pfull[2], pfree[2];
+    uint64_t qfull, qempty, ofull, drain;
     uint32_t tmem;
     int abort, last, unused;
     unsigned long long bad_v;          // drafted slots with non-finite values, this segment
-    int tiles[kMaxLanes], lo[kMaxLanes], nrow[kMaxLanes], len[kMaxLanes], end[kMaxLanes];
+    int tiles[kMaxLanes], lo[kMaxLanes], nodes[kMaxLanes], len[kMaxLanes], end[kMaxLanes];
     int base[kMaxLanes + 1];           // first unit of each lane
     int width;                         // CTAs that share a (lane, head), one per block of query rows
     uint64_t vis[128];                 // drafted slots each column sees
     alignas(16) float m[128];
-    float l[128];
+    float inv[128];                    // 1 / sum
+    int64_t off[128];                  // where each column's output row starts
+    int lse[128];
     float red[4][128];
 };
-static_assert(sizeof(Shared) <= 8192 - 1024, "room for the tables, and for aligning the buffers");
+static_assert(sizeof(Shared) <= 8192, "what the plans leave for it");
 
 struct AttnParams {
     nvfp4_cache c;
@@ -123,6 +125,8 @@ struct AttnParams {
     float2* part_ml;     // [ctas][2][N]
     unsigned* counters;  // [ctas]
     int min_tiles;       // tiles a CTA takes at least (but for the last ones)
+    int per_block;       // rows of a lane per block: as many whole rows (of G columns) as fit N
+    int q_box;           // rows a copy of Q brings (at most per_block)
 };
 
 // -------------------------------------------------------------- tensor cores
@@ -229,6 +233,14 @@ __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, i
         : "memory");
 }
 
+__device__ __forceinline__ void tma_rows(uint32_t dst, const CUtensorMap* map, int x, int head, int row, uint32_t bar)
+{
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        ::"r"(dst), "l"(map), "r"(x), "r"(head), "r"(row), "r"(bar)
+        : "memory");
+}
+
 // ----------------------------------------------------------- bounded waits
 
 // A plain test first: a try_wait costs hundreds of cycles even when the phase is complete.
@@ -322,18 +334,110 @@ __device__ __forceinline__ void read_scores(uint32_t at, float (&x)[CH], bool pl
     }
 }
 
+// ------------------------------------------------------------------- joins
+
+// The parts of a (lane, head) pair's columns, in CTA order: part 0 at row
+// `first` of the workspace, part q > 0 at rest + q step.
+template <int D, int N>
+__device__ __forceinline__ void join_parts(const AttnParams& p, Shared& s, uint8_t* space, int tid, int rows, int np,
+                                        int64_t first, int64_t rest, int64_t step)
+{
+    using L = Plan<D, N>;
+    constexpr int kAllBar = 5, kSoftThreads = L::kSoftThreads;
+    const nvfp4_attn_args& a = p.a;
+    // Maxima and sums of all parts come first, all loads at once, into the (now
+    // idle) space of P; then the weights.
+    float2* ml = reinterpret_cast<float2*>(space);
+    const bool fits = np * rows * 8 <= L::kPBufs * L::kPBytes;
+    if (fits)
+        for (int i = tid; i < np * rows; i += kSoftThreads) {
+            const int q = i / rows, col = i - q * rows;
+            ml[i] = __ldcg(&p.part_ml[(q ? rest + q * step : first) + col]);
+        }
+    any_of(kAllBar, kSoftThreads, false);
+    auto part_of = [&](int q, int col) {
+        return fits ? ml[q * rows + col] : __ldcg(&p.part_ml[(q ? rest + q * step : first) + col]);
+    };
+    if (tid < rows) {
+        float top = kUnseen, sum = 0.f;
+#pragma unroll 8
+        for (int q = 0; q < np; ++q) top = fmaxf(top, part_of(q, tid).x);
+#pragma unroll 8
+        for (int q = 0; q < np; ++q) {
+            const float2 v = part_of(q, tid);
+            const float w = v.x == top ? 1.f : fast_exp2(v.x - top);
+            sum += v.y * w;
+            if (fits) ml[q * rows + tid].x = w;
+        }
+        s.m[tid] = top;
+        s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
+        if (a.lse) a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    }
+    any_of(kAllBar, kSoftThreads, false);
+    constexpr int kQuads = D / 4, kOnce = 4;  // float4 of a row; how many a thread sums at a time
+    for (int i0 = tid; i0 < rows * kQuads; i0 += kOnce * kSoftThreads) {
+        float4 acc[kOnce];
+#pragma unroll
+        for (int z = 0; z < kOnce; ++z) acc[z] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 2
+        for (int q = 0; q < np; ++q) {
+            const float4* src = reinterpret_cast<const float4*>(p.part_o + (q ? rest + q * step : first) * D);
+            float4 v[kOnce];
+#pragma unroll
+            for (int z = 0; z < kOnce; ++z) {
+                const int i = i0 + z * kSoftThreads;
+                if (i < rows * kQuads) v[z] = __ldcg(src + i);
+            }
+#pragma unroll
+            for (int z = 0; z < kOnce; ++z) {
+                const int i = i0 + z * kSoftThreads;
+                if (i < rows * kQuads) {
+                    const int col = i / kQuads;
+                    float w = part_of(q, col).x;
+                    if (!fits) w = w == s.m[col] ? 1.f : fast_exp2(w - s.m[col]);
+                    acc[z].x += w * v[z].x;
+                    acc[z].y += w * v[z].y;
+                    acc[z].z += w * v[z].z;
+                    acc[z].w += w * v[z].w;
+                }
+            }
+        }
+#pragma unroll
+        for (int z = 0; z < kOnce; ++z) {
+            const int i = i0 + z * kSoftThreads;
+            if (i < rows * kQuads) {
+                const int col = i / kQuads, d = i % kQuads * 4;
+                const float inv = s.inv[col];
+                __nv_bfloat162 h0 = __floats2bfloat162_rn(acc[z].x * inv, acc[z].y * inv);
+                __nv_bfloat162 h1 = __floats2bfloat162_rn(acc[z].z * inv, acc[z].w * inv);
+                *reinterpret_cast<uint2*>((uint16_t*)a.out + s.off[col] + d) =
+                    make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
+            }
+        }
+    }
+}
+
+// With 128 columns a call of its own: in line it would cost the softmax loop
+// spills, which go to L2 here (the plans leave L1 no room).
+template <int D, int N>
+__device__ __noinline__ void join_parts_apart(const AttnParams& p, Shared& s, uint8_t* space, int tid, int rows, int np,
+                                              int64_t first, int64_t rest, int64_t step)
+{
+    join_parts<D, N>(p, s, space, tid, rows, np, first, rest, step);
+}
+
 // ---------------------------------------------------------------- the kernel
 
 template <int D, int N>
 __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     attn_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
-                const __grid_constant__ CUtensorMap map_v)
+                const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
     using L = Plan<D, N>;
     // columns of a softmax thread, and those it holds at once
-    constexpr int C = L::kCols, CH = N == 128 ? 16 : C;
+    constexpr int C = L::kCols, CH = N == 128 ? 16 : C, CE = C < 16 ? C : 16;
     constexpr int kSoftWarps = L::kSoftWarps, kSoftThreads = L::kSoftThreads, kLoadWarp = L::kLoadWarp,
-                  kMmaWarp = L::kMmaWarp;
+                  kMmaWarp = L::kMmaWarp, kQWarp = L::kMmaWarp + 1;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
     Shared& s = *reinterpret_cast<Shared*>(sm + L::kOffMisc);
@@ -353,11 +457,11 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&s.sfull[i]), 1);
-            mbar_init(smem_addr(&s.sfree[i]), kSoftWarps);
             mbar_init(smem_addr(&s.pfull[i]), kSoftWarps);
             mbar_init(smem_addr(&s.pfree[i]), 1);
         }
-        mbar_init(smem_addr(&s.qfull), kSoftWarps);
+        mbar_init(smem_addr(&s.qfull), 1);
+        mbar_init(smem_addr(&s.qempty), 1);
         mbar_init(smem_addr(&s.ofull), 1);
         mbar_init(smem_addr(&s.drain), 1);
         s.abort = 0;
@@ -372,7 +476,12 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     if (warp == kLoadWarp && lane == 0) {
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
         asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
     }
+    // columns of Q that no copy writes stay zero
+    for (int i = tid; i < L::kQBytes / 16; i += L::kThreads)
+        *reinterpret_cast<uint4*>(sm + L::kOffQ + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_async();
     pdl_begin();
     // the lanes: rows, lengths, tiles
     if (tid < kMaxLanes) {
@@ -390,7 +499,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             }
         }
         s.lo[tid] = lo;
-        s.nrow[tid] = (hi - lo) * G;
+        s.nodes[tid] = hi - lo;
         s.len[tid] = len;
         s.end[tid] = end;
         s.tiles[tid] = tiles;
@@ -399,7 +508,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     if (warp == 0) {
         // prefix sums of units and the widest lane, two lanes per thread
         const int x0 = s.tiles[2 * lane] * c.kv_heads, x1 = s.tiles[2 * lane + 1] * c.kv_heads;
-        int incl = x0 + x1, most = max(s.nrow[2 * lane], s.nrow[2 * lane + 1]);
+        int incl = x0 + x1, most = max(s.nodes[2 * lane], s.nodes[2 * lane + 1]);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, off);
@@ -409,7 +518,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         s.base[2 * lane] = incl - x0 - x1;
         s.base[2 * lane + 1] = incl - x1;
         if (lane == 31) s.base[kMaxLanes] = incl;
-        if (lane == 0) s.width = max(1, (most + N - 1) / N);
+        if (lane == 0) s.width = max(1, (most + p.per_block - 1) / p.per_block);
     }
     fence_after();
     __syncthreads();
@@ -435,7 +544,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * N >= s.nrow[g.b]) continue;
+            if (blk * p.per_block >= s.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
             const int end = s.end[g.b];
@@ -481,6 +590,28 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             for (int q = max(0, done - L::kRing); q < done; ++q)
                 warp_wait(smem_addr(&s.full[q % L::kRing]), (q / L::kRing) & 1);
         }
+    } else if (warp == kQWarp) {
+        // ---- queries: the block's rows x the pair's G heads, as the columns' order wants them
+        int seg = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s, c.lanes, u, u1);
+            u += g.t1 - g.t0;
+            if (blk * p.per_block >= s.nodes[g.b]) continue;
+            if (seg > 0) ok = waitw(smem_addr(&s.qempty), (seg - 1) & 1, abort);
+            if (ok && lane == 0) {
+                const uint32_t bar = smem_addr(&s.qfull);
+                mbar_expect_tx(bar, (uint32_t)(p.q_box * G * D * 2));
+                for (int x = 0; x < D / 64; ++x)
+                    tma_rows(qbuf + x * N * 128, &map_q, x * 64, g.h * G, s.lo[g.b] + blk * p.per_block, bar);
+            }
+            __syncwarp();
+            ++seg;
+        }
+        if (seg > 0) {
+            if (!ok && lane == 0) give_up(abort);
+            warp_wait(smem_addr(&s.qfull), (seg - (ok ? 1 : 2)) & 1);  // the last copy has landed
+        }
     } else if (warp == kMmaWarp) {
         // ---- the products
         const uint32_t lead = elect();
@@ -492,14 +623,15 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * N >= s.nrow[g.b]) continue;
+            if (blk * p.per_block >= s.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
             fence_after();
             for (int t = 0; ok && t <= n; ++t) {
                 if (t < n) {  // S of tile t
                     const int T = done + t, sb = T & 1;
-                    if (T >= 2) ok = waitw(smem_addr(&s.sfree[sb]), ((T >> 1) - 1) & 1, abort);
+                    // its buffer is free: S of tile t - 2 was read before that tile's
+                    // weights were announced, and O of tile t - 2 waited for those
                     for (int e = 0; ok && e < L::kPer; ++e) {
                         const int q = idx + pos_k(t) * L::kPer + e, slot = q % L::kRing;
                         ok = waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort);
@@ -513,7 +645,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                                     desc_k(qbuf + (e * L::kAtoms + x) * N * 128 + k * 32), kIdS, (e | x | k) != 0);
                         commit(lead, smem_addr(&s.empty[slot]));
                     }
-                    if (ok) commit(lead, smem_addr(&s.sfull[sb]));
+                    if (ok) {
+                        commit(lead, smem_addr(&s.sfull[sb]));
+                        if (t == n - 1) commit(lead, smem_addr(&s.qempty));
+                    }
                 }
                 if (ok && t > 0) {  // O of tile t - 1
                     const int T = done + t - 1, pb = T % L::kPBufs;
@@ -558,37 +693,27 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         for (int u = u0; u < u1;) {
             const Segment g = segment_at(s, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * N >= s.nrow[g.b]) continue;
+            if (blk * p.per_block >= s.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
-            const int len = s.len[g.b], end = s.end[g.b], rows = min(N, s.nrow[g.b] - blk * N), lo = s.lo[g.b];
+            const int len = s.len[g.b], end = s.end[g.b], lo = s.lo[g.b];
+            const int rows = min(p.per_block, s.nodes[g.b] - blk * p.per_block) * G;  // columns in use
             const int32_t* trow = c.table + (int64_t)g.b * c.max_pages;
             int pg = g.t0 * kTile + srow < end ? trow[(g.t0 * kTile + srow) >> shift] : -1;
-            // Q: row r of the block is query row lo + r / G, head h G + r % G
-            for (int i = tid; i < N * D / 8; i += kSoftThreads) {
-                const int r = i / (D / 8), ch = i % (D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int rr = blk * N + r;
-                    v = *reinterpret_cast<const uint4*>((const uint16_t*)a.q + (int64_t)(lo + rr / G) * a.ldq +
-                                                        (int64_t)(g.h * G + rr % G) * D + ch * 8);
-                }
-                *reinterpret_cast<uint4*>(sm + L::kOffQ + (ch >> 3) * N * 128 + r * 128 + (((ch & 7) ^ (r & 7)) << 4)) = v;
-            }
+            // column j of the block is row lo + i, i = blk per_block + j / G, head h G + j % G
             if (tid < N) {
                 uint64_t w = 0;
                 if (tid < rows) {
-                    const int i = (blk * N + tid) / G, T = s.nrow[g.b] / G;
+                    const int i = blk * p.per_block + tid / G, head = g.h * G + tid % G, T = s.nodes[g.b];
                     w = a.mask ? a.mask[lo + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
                     if (T < 64) w &= (1ull << T) - 1;
+                    s.off[tid] = (int64_t)(lo + i) * a.ldo + (int64_t)head * D;
+                    s.lse[tid] = (lo + i) * a.q_heads + head;
                 }
                 s.vis[tid] = w;
                 s.m[tid] = kUnseen;
                 if (tid == 0) s.bad_v = 0;
             }
-            fence_async();
-            fence_before();
             any_of(kAllBar, kSoftThreads, false);
-            if (lane == 0) mbar_arrive(smem_addr(&s.qfull));
 
             float l[C];
 #pragma unroll
@@ -680,7 +805,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                                                          fmaxf(s.red[2][col], s.red[3][col])));
                     any_of(bar, 128, false);
                 }
-                if (T >= L::kPBufs)
+                // (two buffers: S of this tile was issued after O of the tile before the
+                // last, so once S is there the weights of that tile are done with)
+                if (L::kPBufs == 1 && T > 0)
                     fail = fail || !waitw(smem_addr(&s.pfree[pb]), ((T / L::kPBufs) - 1) & 1, abort);
                 // weights
                 uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
@@ -712,10 +839,6 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                         *reinterpret_cast<uint4*>(prow + ((c0 + i0 + i) >> 3) * (kTile * 16)) = v;
                     }
                 }
-                // the scores' buffer may be filled again
-                fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s.sfree[sb]));
                 if (!plain) {
                     // V rows that are nobody's slot: zero; of drafted slots: their non-finite values
                     for (int e = 0; e < L::kPer; ++e) {
@@ -772,61 +895,60 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fail = true;
                 break;
             }
-            if (tid < N) s.l[tid] = (s.red[0][tid] + s.red[1][tid]) + (s.red[2][tid] + s.red[3][tid]);
-            any_of(kAllBar, kSoftThreads, false);
-            // O^T: this thread's value row(s), its half of the columns
             const bool whole = g.t0 == 0 && g.t1 == s.tiles[g.b];
             const int pslot = g.first <= u0 ? 0 : 1;
             const int64_t part = (int64_t)blockIdx.x * 2 + pslot;
+            if (tid < N) {
+                const float sum = (s.red[0][tid] + s.red[1][tid]) + (s.red[2][tid] + s.red[3][tid]);
+                s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
+                if (tid < rows) {
+                    if (!whole)
+                        p.part_ml[part * N + tid] = make_float2(s.m[tid], sum);
+                    else if (a.lse)
+                        a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (s.m[tid] + log2f(sum)) * 0.6931471805599453f;
+                }
+            }
+            any_of(kAllBar, kSoftThreads, false);
+            // O^T: this thread's value row(s), its share of the columns
             const uint64_t badv = s.bad_v;
 #pragma unroll 1
             for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
                 const int d = blkd * 128 + srow;
+                float* po = p.part_o + (part * N + c0) * D + d;
+                __nv_bfloat16* out = (__nv_bfloat16*)a.out + d;
 #pragma unroll 1
-                for (int i0 = 0; i0 < C; i0 += 8) {
-                    float o[8];
-                    tm_ld8(tm_o + blkd * N + c0 + i0 + lanebits, o);
-                    tm_wait_ld();
+                for (int i0 = 0; i0 < C && c0 + i0 < rows; i0 += CE) {
+                    float o[CE];
+                    tm_ld<CE>(tm_o + blkd * N + c0 + i0 + lanebits, o);
                     if (d >= D) continue;
                     if (badv) {
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
+#pragma unroll 1
+                        for (int j = 0; j < CE; ++j) {
                             for (uint64_t w = badv & s.vis[c0 + i0 + j]; w; w &= w - 1) {
                                 const int sl2 = len + __ffsll(w) - 1;
                                 const int pgv = trow[sl2 >> shift];
                                 const float v = __bfloat162float(
                                     ((const __nv_bfloat16*)c.v)[((((int64_t)a.layer * c.pages + pgv) * c.kv_heads + g.h) *
                                                                      c.page_size + (sl2 & (c.page_size - 1))) * D + d]);
-                                if (!isfinite(v)) o[j] += v;
+#pragma unroll
+                                for (int z = 0; z < CE; ++z)
+                                    if (z == j && !isfinite(v)) o[z] += v;
                             }
                         }
                     }
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < CE; ++j) {
                         const int col = c0 + i0 + j;
-                        if (col >= rows) break;
-                        if (whole) {
-                            const int rr = blk * N + col;
-                            const float sum = s.l[col];
-                            ((__nv_bfloat16*)a.out)[(int64_t)(lo + rr / G) * a.ldo + (int64_t)(g.h * G + rr % G) * D + d] =
-                                __float2bfloat16(sum == 0.f ? 0.f : o[j] / sum);
-                        } else {
-                            p.part_o[(part * N + col) * D + d] = o[j];
+                        if (col < rows) {
+                            if (whole)
+                                out[s.off[col]] = __float2bfloat16(o[j] * s.inv[col]);
+                            else
+                                po[(i0 + j) * D] = o[j];
                         }
                     }
                 }
             }
             fence_before();
-            if (tid < rows) {
-                const float sum = s.l[tid];
-                if (!whole) {
-                    p.part_ml[part * N + tid] = make_float2(s.m[tid], sum);
-                } else if (a.lse) {
-                    const int rr = blk * N + tid;
-                    a.lse[(int64_t)(lo + rr / G) * a.q_heads + g.h * G + rr % G] =
-                        sum == 0.f ? -INFINITY : (s.m[tid] + log2f(sum)) * 0.6931471805599453f;
-                }
-            }
             if (!whole) {
                 // the pair's CTAs: those of the groups that hold its first to its last unit
                 const int last_u = g.first + s.tiles[g.b] - 1;
@@ -838,46 +960,11 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 any_of(kAllBar, kSoftThreads, false);
                 if (s.last) {
                     const int lo_slot = (int)((int64_t)units * glo / groups) >= g.first ? 0 : 1;
-                    auto slot_of = [&](int q) { return (int64_t)(q * width + blk) * 2 + (q == glo ? lo_slot : 0); };
-                    if (tid < rows) {
-                        float top = kUnseen, sum = 0.f;
-                        for (int q = glo; q <= ghi; ++q) top = fmaxf(top, __ldcg(&p.part_ml[slot_of(q) * N + tid]).x);
-                        for (int q = glo; q <= ghi; ++q) {
-                            const float2 ml = __ldcg(&p.part_ml[slot_of(q) * N + tid]);
-                            sum += ml.y * (ml.x == top ? 1.f : fast_exp2(ml.x - top));
-                        }
-                        s.m[tid] = top;
-                        s.l[tid] = sum;
-                        if (a.lse) {
-                            const int rr = blk * N + tid;
-                            a.lse[(int64_t)(lo + rr / G) * a.q_heads + g.h * G + rr % G] =
-                                sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-                        }
-                    }
-                    any_of(kAllBar, kSoftThreads, false);
-                    for (int i = tid; i < rows * (D / 4); i += kSoftThreads) {
-                        const int col = i / (D / 4), d = i % (D / 4) * 4;
-                        const float top = s.m[col], sum = s.l[col];
-                        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-                        for (int q = glo; q <= ghi; ++q) {
-                            const int64_t at = slot_of(q) * N + col;
-                            const float m = __ldcg(&p.part_ml[at]).x;
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(p.part_o + at * D + d));
-                            const float w = m == top ? 1.f : fast_exp2(m - top);
-                            acc.x += w * v.x;
-                            acc.y += w * v.y;
-                            acc.z += w * v.z;
-                            acc.w += w * v.w;
-                        }
-                        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-                        __nv_bfloat162 h0 = __floats2bfloat162_rn(acc.x * inv, acc.y * inv);
-                        __nv_bfloat162 h1 = __floats2bfloat162_rn(acc.z * inv, acc.w * inv);
-                        const int rr = blk * N + col;
-                        *reinterpret_cast<uint2*>((uint16_t*)a.out + (int64_t)(lo + rr / G) * a.ldo +
-                                                  (int64_t)(g.h * G + rr % G) * D + d) =
-                            make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
-                    }
+                    const int64_t rest = (int64_t)(glo * width + blk) * 2 * N, step = (int64_t)width * 2 * N;
+                    if constexpr (N == 128)
+                        join_parts_apart<D, N>(p, s, sm + L::kOffP, tid, rows, ghi - glo + 1, rest + lo_slot * N, rest, step);
+                    else
+                        join_parts<D, N>(p, s, sm + L::kOffP, tid, rows, ghi - glo + 1, rest + lo_slot * N, rest, step);
                     if (tid == 0) p.counters[glo * width + blk] = 0u;
                 }
             }
@@ -933,6 +1020,19 @@ int page_map(EncodeFn encode, const nvfp4_cache& c, void* pool, int layer, CUten
     return r == CUDA_SUCCESS ? NVFP4_OK : fail_cuda(cudaErrorInvalidValue);
 }
 
+// The query rows as [rows][q_heads][head_dim], fetched 64 values x g heads x q_box rows at a time.
+int query_map(EncodeFn encode, const nvfp4_attn_args& a, int g, int q_box, CUtensorMap* map)
+{
+    const cuuint64_t dims[3] = {(cuuint64_t)a.cache->head_dim, (cuuint64_t)a.q_heads, (cuuint64_t)a.rows};
+    const cuuint64_t strides[2] = {(cuuint64_t)a.cache->head_dim * 2, (cuuint64_t)a.ldq * 2};
+    const cuuint32_t box[3] = {64, (cuuint32_t)g, (cuuint32_t)q_box};
+    const cuuint32_t step[3] = {1, 1, 1};
+    const CUresult r = encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(a.q), dims, strides, box, step,
+                              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                              CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? NVFP4_OK : fail_cuda(cudaErrorInvalidValue);
+}
+
 // Query rows per block: what one lane is expected to have, at most 128.
 int block_rows(int max_nodes, int rows, int g)
 {
@@ -954,7 +1054,8 @@ Workspace workspace(int head_dim, int sms)
 }
 
 template <int D, int N>
-int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t stream)
+int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, int sms,
+                   cudaStream_t stream)
 {
     using L = Plan<D, N>;
     constexpr int kBytes = L::kOffMisc + (int)sizeof(Shared) + 1024;
@@ -967,18 +1068,19 @@ int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap
         NVFP4_CUDA_TRY(cudaFuncSetAttribute(attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
         ready.fetch_or(1ull << dev);
     }
-    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(L::kThreads), kBytes, stream, p, mk, mv));
+    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
     return NVFP4_OK;
 }
 
 template <int D>
-int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, int sms, cudaStream_t stream)
+int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, int sms,
+               cudaStream_t stream)
 {
     switch (n) {
-    case 16: return launch_variant<D, 16>(p, mk, mv, sms, stream);
-    case 32: return launch_variant<D, 32>(p, mk, mv, sms, stream);
-    case 64: return launch_variant<D, 64>(p, mk, mv, sms, stream);
-    default: return launch_variant<D, 128>(p, mk, mv, sms, stream);
+    case 16: return launch_variant<D, 16>(p, mk, mv, mq, sms, stream);
+    case 32: return launch_variant<D, 32>(p, mk, mv, mq, sms, stream);
+    case 64: return launch_variant<D, 64>(p, mk, mv, mq, sms, stream);
+    default: return launch_variant<D, 128>(p, mk, mv, mq, sms, stream);
     }
 }
 
@@ -1008,7 +1110,7 @@ int validate_attn(const nvfp4_attn_args* a)
     const int64_t width = (int64_t)a->q_heads * c->head_dim;
     if (a->layer < 0 || a->layer >= c->layers || a->q_heads < 1 || a->q_heads % c->kv_heads ||
         a->q_heads > 32 * c->kv_heads || a->max_nodes < 1 || a->ldq < width || a->ldo < width ||
-        a->ldq > ((int64_t)1 << 40) || a->ldo > ((int64_t)1 << 40))
+        a->ldq > ((int64_t)1 << 38) || a->ldo > ((int64_t)1 << 40))
         return NVFP4_ERR_SHAPE;
     if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace) || (a->ldq & 7) || (a->ldo & 7) ||
         (((uintptr_t)a->row_start | (uintptr_t)a->lse) & 3) || ((uintptr_t)a->mask & 7))
@@ -1037,12 +1139,17 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     if (st == NVFP4_OK) st = page_map(encode, p.c, p.c.k, a->layer, &mk);
     if (st == NVFP4_OK) st = page_map(encode, p.c, p.c.v, a->layer, &mv);
     if (st != NVFP4_OK) return st;
-    int n = block_rows(a->max_nodes, a->rows, a->q_heads / p.c.kv_heads);
-    // every block of a lane needs a CTA, whatever the hint says
-    while (n < 128 && (a->rows * (a->q_heads / p.c.kv_heads) + n - 1) / n > sms) n *= 2;
-    return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, sms, stream)
-           : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, sms, stream)
-                                 : launch_dim<256>(n, p, mk, mv, sms, stream);
+    // at least one whole row per block, so a lane has at most 64 blocks
+    const int g = a->q_heads / p.c.kv_heads, n = block_rows(a->max_nodes, a->rows, g);
+    p.per_block = n / g;
+    p.q_box = p.per_block < a->rows ? p.per_block : a->rows;
+    CUtensorMap mq;
+    st = query_map(encode, *a, g, p.q_box, &mq);
+    if (st != NVFP4_OK) return st;
+    if (sms < NVFP4_ATTN_MAX_ROWS) return fail_cuda(cudaErrorInvalidDevice);
+    return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, mq, sms, stream)
+           : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, mq, sms, stream)
+                                 : launch_dim<256>(n, p, mk, mv, mq, sms, stream);
 }
 
 }  // namespace nvfp4
