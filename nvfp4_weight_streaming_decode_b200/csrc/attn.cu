@@ -81,17 +81,14 @@ struct Plan {
     static constexpr int kOffP = kRing * kEntry;
     static constexpr int kOffQ = kOffP + kPBufs * kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
-    // Softmax warps come in groups of four (32 slots each) that share the columns
-    // out; 128 columns take four groups, because a thread with 64 of them spills.
-    static constexpr int kGroups = N == 128 ? 4 : 2;
-    static constexpr int kCols = N / kGroups;                // columns per softmax thread
-    static constexpr int kSoftWarps = 4 * kGroups, kSoftThreads = 32 * kSoftWarps;
+    // Softmax warps come in two groups of four (32 slots each), half the columns each.
+    static constexpr int kCols = N / 2;                      // columns per softmax thread
+    static constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
     static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
     static constexpr int kThreads = kSoftThreads + 128;      // the last group: pages, products, queries, an idle warp
     // Registers: kThreads x kLaunch at launch = softmax threads x kSoft + 128 x kRest
     // (what one side gains the other gives up, or the gaining side would wait forever).
-    static constexpr int kLaunch = kGroups == 4 ? 96 : 168, kSoft = kGroups == 4 ? 104 : 208,
-                         kRest = kGroups == 4 ? 64 : 88;
+    static constexpr int kLaunch = 168, kSoft = 208, kRest = 88;
     static_assert(kThreads * kLaunch == kSoftThreads * kSoft + 128 * kRest && kThreads * kLaunch <= 65536, "registers");
     static constexpr int kOBlocks = D > 128 ? 2 : 1;         // 128-row blocks of O^T
     // loads and products take entries in one order, so a tile of V beside one entry of K is enough to go on
@@ -110,7 +107,7 @@ struct Shared {  // at kOffMisc
     int base[kMaxLanes + 1];           // first unit of each lane
     int width;                         // CTAs that share a (lane, head), one per block of query rows
     uint64_t vis[128];                 // drafted slots each column sees
-    alignas(16) float m[128];
+    alignas(16) float neg_m[128];      // each column's reference, negated
     float inv[128];                    // 1 / sum
     int64_t off[128];                  // where each column's output row starts
     int lse[128];
@@ -293,6 +290,37 @@ __device__ __forceinline__ float fast_exp2(float x)
     return y;
 }
 
+// Pairs of FP32 in one instruction: half the issue slots of the softmax.
+typedef unsigned long long f32x2;
+__device__ __forceinline__ f32x2 pair(float a, float b)
+{
+    f32x2 r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpair(f32x2 v, float& a, float& b)
+{
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ f32x2 fma2(f32x2 a, f32x2 b, f32x2 c)
+{
+    f32x2 r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ f32x2 add2(f32x2 a, f32x2 b)
+{
+    f32x2 r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ float max3(float a, float b, float c)
+{
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+
 // ------------------------------------------------------------- the schedule
 
 // Units are (lane, cached head, tile), lane by lane; a group of `width` CTAs
@@ -321,17 +349,97 @@ __device__ __forceinline__ Segment segment_at(const Shared& s, int lanes, int u,
 __device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
 
-// CH scores of this thread's slot from tensor memory, scaled and masked unless
-// the whole warp's slots are seen by every row (`plain`); `all`: this slot is.
-template <int CH>
-__device__ __forceinline__ void read_scores(uint32_t at, float (&x)[CH], bool plain, bool all, uint64_t bit, float sl,
-                                            const uint64_t* vis)
+// C scores of this thread's slot from tensor memory, as log2 weights against the
+// references: x = s scale log2(e) - m.  Masked ones are -inf, whatever the
+// scale's sign.  `plain`: the whole warp's slots are seen by every row; `all`:
+// this slot is.
+template <int C>
+__device__ __forceinline__ void read_scores(uint32_t at, float (&x)[C], bool plain, bool all, uint64_t bit, float sl,
+                                            const uint64_t* vis, const float* neg_m)
 {
-    tm_ld<CH>(at, x);
+    tm_ld<C>(at, x);
+    const f32x2 f = pair(sl, sl);
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_m + i);
+        unpair(fma2(pair(x[i], x[i + 1]), f, m.x), x[i], x[i + 1]);
+        unpair(fma2(pair(x[i + 2], x[i + 3]), f, m.y), x[i + 2], x[i + 3]);
+    }
     if (!plain) {
 #pragma unroll
-        for (int i = 0; i < CH; ++i) x[i] = all || (vis[i] & bit) ? x[i] * sl : -INFINITY;
+        for (int i = 0; i < C; ++i)
+            if (!all && !(vis[i] & bit)) x[i] = -INFINITY;
     }
+}
+
+// ------------------------------------------------------------ new references
+
+// This group of four warps gives its columns the maxima of this tile's scores as
+// references where those are higher, and scales its sums and O^T so far.
+template <int D, int N>
+__device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bool plain, bool all, uint64_t bit, float sl,
+                                     int c0, int quad, int lane, int bar, bool started, f32x2 (&l)[N / 4],
+                                     uint32_t pfree, uint32_t parity, volatile int* abort, bool& fail)
+{
+    using L = Plan<D, N>;
+    constexpr int C = L::kCols;
+#pragma unroll 1
+    for (int i0 = 0; i0 < C; i0 += 8) {
+        float x[8];
+        tm_ld8(at_s + i0, x);
+        tm_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float v = plain || all || (s.vis[c0 + i0 + i] & bit) ? x[i] * sl : -INFINITY;
+#pragma unroll
+            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            if (lane == 0) s.red[quad][c0 + i0 + i] = v;
+        }
+    }
+    any_of(bar, 128, false);
+    // O^T so far, once every product before this tile is done
+    if (started) {
+        fail = fail || !waitw(pfree, parity, abort);
+        fence_after();
+    }
+#pragma unroll
+    for (int i0 = 0; i0 < C; i0 += 8) {
+        float down[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int col = c0 + i0 + j;
+            const float was = -s.neg_m[col];
+            float now = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+            now = fmaxf(now, was);
+            down[j] = was == now ? 1.f : fast_exp2(was - now);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            float v, w;
+            unpair(l[(i0 + j) / 2], v, w);
+            l[(i0 + j) / 2] = pair(v * down[j], w * down[j + 1]);
+        }
+        if (started) {
+#pragma unroll
+            for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
+                float o[8];
+                const uint32_t at = at_o + blkd * N + i0;
+                tm_ld8(at, o);
+                tm_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) o[j] *= down[j];
+                tm_st8(at, o);
+                tm_wait_st();
+            }
+        }
+    }
+    fence_before();
+    any_of(bar, 128, false);  // every thread has read the old references
+    const int col = c0 + quad * 32 + lane;
+    if (quad * 32 + lane < C)
+        s.neg_m[col] = -fmaxf(-s.neg_m[col], fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
+                                                   fmaxf(s.red[2][col], s.red[3][col])));
+    any_of(bar, 128, false);
 }
 
 // ------------------------------------------------------------------- joins
@@ -369,7 +477,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, Shared& s, uint8
             sum += v.y * w;
             if (fits) ml[q * rows + tid].x = w;
         }
-        s.m[tid] = top;
+        s.neg_m[tid] = -top;
         s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
         if (a.lse) a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
     }
@@ -394,7 +502,7 @@ __device__ __forceinline__ void join_parts(const AttnParams& p, Shared& s, uint8
                 if (i < rows * kQuads) {
                     const int col = i / kQuads;
                     float w = part_of(q, col).x;
-                    if (!fits) w = w == s.m[col] ? 1.f : fast_exp2(w - s.m[col]);
+                    if (!fits) w = w == -s.neg_m[col] ? 1.f : fast_exp2(w + s.neg_m[col]);
                     acc[z].x += w * v[z].x;
                     acc[z].y += w * v[z].y;
                     acc[z].z += w * v[z].z;
@@ -434,8 +542,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
     using L = Plan<D, N>;
-    // columns of a softmax thread, and those it holds at once
-    constexpr int C = L::kCols, CH = N == 128 ? 16 : C, CE = C < 16 ? C : 16;
+    // columns of a softmax thread, and those of O it reads at once
+    constexpr int C = L::kCols, CE = C < 16 ? C : 16;
     constexpr int kSoftWarps = L::kSoftWarps, kSoftThreads = L::kSoftThreads, kLoadWarp = L::kLoadWarp,
                   kMmaWarp = L::kMmaWarp, kQWarp = L::kMmaWarp + 1;
     extern __shared__ uint8_t raw[];
@@ -710,14 +818,14 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                     s.lse[tid] = (lo + i) * a.q_heads + head;
                 }
                 s.vis[tid] = w;
-                s.m[tid] = kUnseen;
+                s.neg_m[tid] = -kUnseen;
                 if (tid == 0) s.bad_v = 0;
             }
             any_of(kAllBar, kSoftThreads, false);
 
-            float l[C];
+            f32x2 l[C / 2];
 #pragma unroll
-            for (int i = 0; i < C; ++i) l[i] = 0.f;
+            for (int i = 0; i < C / 2; ++i) l[i] = 0;
             bool stop = false;
             for (int t = 0; t < n; ++t) {
                 const int T = done + t, sb = T & 1, pb = T % L::kPBufs;
@@ -726,84 +834,26 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 if (slot < end && !valid) atomicOr(&g_attn_status, kBadPage);
                 const bool plain = __all_sync(0xffffffffu, valid && slot < len);
                 if (t + 1 < n) pg = slot + kTile < end ? trow[(slot + kTile) >> shift] : -1;
-                // Scores times f are in units of log2; a masked one is -inf whatever
-                // the scale's sign, so where there is a mask the scale goes first.
-                const float f = plain ? sl : 1.f;
                 const bool all = slot < len && valid;
                 const uint64_t bit = valid && slot >= len ? 1ull << (slot - len) : 0ull;
+                const uint32_t at_s = tm_s + sb * N + c0 + lanebits;
                 fail = fail || !waitw(smem_addr(&s.sfull[sb]), (T >> 1) & 1, abort);
                 fence_after();
+                float x[C];
+                read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
                 // over the reference by more than the headroom?
-                float x[CH];
-                float over = -INFINITY;
+                float over = fmaxf(x[0], x[1]);
 #pragma unroll
-                for (int i0 = 0; i0 < C; i0 += CH) {
-                    read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
-#pragma unroll
-                    for (int i = 0; i < CH; i += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&s.m[c0 + i0 + i]);
-                        over = fmaxf(fmaxf(over, fmaf(x[i], f, -m.x)), fmaf(x[i + 1], f, -m.y));
-                        over = fmaxf(fmaxf(over, fmaf(x[i + 2], f, -m.z)), fmaf(x[i + 3], f, -m.w));
-                    }
-                }
+                for (int i = 2; i < C; i += 2) over = max3(over, x[i], x[i + 1]);
                 if (any_of(bar, 128, over > kHeadroom || fail)) {
                     if (any_of(bar, 128, fail)) {
                         if (lane == 0) give_up(abort);
                         stop = true;
                         break;
                     }
-                    // new references: the columns' maxima over this tile, where they are higher
-#pragma unroll
-                    for (int i0 = 0; i0 < C; i0 += CH) {
-                        if (C > CH)
-                            read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
-#pragma unroll
-                        for (int i = 0; i < CH; ++i) {
-                            float v = x[i] * f;
-#pragma unroll
-                            for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-                            if (lane == 0) s.red[quad][c0 + i0 + i] = v;
-                        }
-                    }
-                    any_of(bar, 128, false);
-                    // O^T so far, once every product before this tile is done
-                    if (t > 0) {
-                        const int Tp = T - 1;
-                        fail = !waitw(smem_addr(&s.pfree[Tp % L::kPBufs]), (Tp / L::kPBufs) & 1, abort);
-                        fence_after();
-                    }
-#pragma unroll
-                    for (int i0 = 0; i0 < C; i0 += 8) {
-                        float down[8];
-#pragma unroll
-                        for (int j = 0; j < 8; ++j) {
-                            const int i = i0 + j, col = c0 + i;
-                            const float was = s.m[col];
-                            float now = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-                            now = fmaxf(now, was);
-                            down[j] = was == now ? 1.f : fast_exp2(was - now);
-                            l[i] *= down[j];
-                        }
-                        if (t > 0) {
-#pragma unroll
-                            for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
-                                float o[8];
-                                const uint32_t at = tm_o + blkd * N + c0 + i0 + lanebits;
-                                tm_ld8(at, o);
-                                tm_wait_ld();
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) o[j] *= down[j];
-                                tm_st8(at, o);
-                                tm_wait_st();
-                            }
-                        }
-                    }
-                    fence_before();
-                    any_of(bar, 128, false);  // every thread has read the old references
-                    for (int col = c0 + srow; col < c0 + C; col += 128)
-                        s.m[col] = fmaxf(s.m[col], fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
-                                                         fmaxf(s.red[2][col], s.red[3][col])));
-                    any_of(bar, 128, false);
+                    rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
+                               smem_addr(&s.pfree[(T + L::kPBufs - 1) % L::kPBufs]), ((T - 1) / L::kPBufs) & 1, abort, fail);
+                    read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
                 }
                 // (two buffers: S of this tile was issued after O of the tile before the
                 // last, so once S is there the weights of that tile are done with)
@@ -812,32 +862,16 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 // weights
                 uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
 #pragma unroll
-                for (int i0 = 0; i0 < C; i0 += CH) {
-                    if (C > CH)
-                        read_scores<CH>(tm_s + sb * N + c0 + i0 + lanebits, x, plain, all, bit, sl, s.vis + c0 + i0);
+                for (int i = 0; i < C; i += 8) {
+                    uint32_t w[4];
 #pragma unroll
-                    for (int i = 0; i < CH; i += 4) {
-                        const float4 m = *reinterpret_cast<const float4*>(&s.m[c0 + i0 + i]);
-                        x[i] = fast_exp2(fmaf(x[i], f, -m.x));
-                        x[i + 1] = fast_exp2(fmaf(x[i + 1], f, -m.y));
-                        x[i + 2] = fast_exp2(fmaf(x[i + 2], f, -m.z));
-                        x[i + 3] = fast_exp2(fmaf(x[i + 3], f, -m.w));
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) l[i0 + i + j] += x[i + j];
+                    for (int j = 0; j < 4; ++j) {
+                        const float y0 = fast_exp2(x[i + 2 * j]), y1 = fast_exp2(x[i + 2 * j + 1]);
+                        l[i / 2 + j] = add2(l[i / 2 + j], pair(y0, y1));
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
+                        w[j] = *reinterpret_cast<const uint32_t*>(&h);
                     }
-#pragma unroll
-                    for (int i = 0; i < CH; i += 8) {
-                        uint4 v;
-                        __nv_bfloat162 h0 = __floats2bfloat162_rn(x[i], x[i + 1]);
-                        __nv_bfloat162 h1 = __floats2bfloat162_rn(x[i + 2], x[i + 3]);
-                        __nv_bfloat162 h2 = __floats2bfloat162_rn(x[i + 4], x[i + 5]);
-                        __nv_bfloat162 h3 = __floats2bfloat162_rn(x[i + 6], x[i + 7]);
-                        v.x = *reinterpret_cast<uint32_t*>(&h0);
-                        v.y = *reinterpret_cast<uint32_t*>(&h1);
-                        v.z = *reinterpret_cast<uint32_t*>(&h2);
-                        v.w = *reinterpret_cast<uint32_t*>(&h3);
-                        *reinterpret_cast<uint4*>(prow + ((c0 + i0 + i) >> 3) * (kTile * 16)) = v;
-                    }
+                    *reinterpret_cast<uint4*>(prow + ((c0 + i) >> 3) * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
                 }
                 if (!plain) {
                     // V rows that are nobody's slot: zero; of drafted slots: their non-finite values
@@ -882,11 +916,18 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             // the columns' sums
             if (!stop) {
 #pragma unroll
-                for (int i = 0; i < C; ++i) {
-                    float v = l[i];
+                for (int i = 0; i < C / 2; ++i) {
+                    float v, w;
+                    unpair(l[i], v, w);
 #pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
-                    if (lane == 0) s.red[quad][c0 + i] = v;
+                    for (int o = 16; o > 0; o >>= 1) {
+                        v += __shfl_xor_sync(0xffffffffu, v, o);
+                        w += __shfl_xor_sync(0xffffffffu, w, o);
+                    }
+                    if (lane == 0) {
+                        s.red[quad][c0 + 2 * i] = v;
+                        s.red[quad][c0 + 2 * i + 1] = w;
+                    }
                 }
                 fail = fail || !waitw(smem_addr(&s.ofull), seg & 1, abort);
                 fence_after();
@@ -903,9 +944,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 if (tid < rows) {
                     if (!whole)
-                        p.part_ml[part * N + tid] = make_float2(s.m[tid], sum);
+                        p.part_ml[part * N + tid] = make_float2(-s.neg_m[tid], sum);
                     else if (a.lse)
-                        a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (s.m[tid] + log2f(sum)) * 0.6931471805599453f;
+                        a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (log2f(sum) - s.neg_m[tid]) * 0.6931471805599453f;
                 }
             }
             any_of(kAllBar, kSoftThreads, false);
