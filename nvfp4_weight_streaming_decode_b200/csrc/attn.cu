@@ -20,8 +20,8 @@
 //
 // Split: the tiles of all (lane, cached head) pairs form one line that the
 // grid's CTAs share evenly (ragged lanes balance by themselves).  A pair cut
-// between CTAs leaves partial (m, l, O) in the workspace, and the last CTA to
-// finish joins them in CTA order.  Lanes with more than N query rows have
+// between CTAs leaves partial (m, l, O) in the workspace, and a second kernel
+// joins them in CTA order.  Lanes with more than N query rows have
 // their blocks on neighbouring CTAs in step, so that the second reader of a
 // tile finds it in L2.
 //
@@ -96,16 +96,22 @@ struct Plan {
     static_assert(2 * N + kOBlocks * N <= 512, "tensor memory");
 };
 
+// What the schedule goes by.
+struct Lanes {
+    int tiles[kMaxLanes], lo[kMaxLanes], nodes[kMaxLanes], len[kMaxLanes], end[kMaxLanes];
+    int base[kMaxLanes + 1];  // first unit of each lane
+    int width;                // CTAs that share a (lane, head), one per block of query rows
+    int groups;               // of `width` CTAs, that share the units
+};
+
 struct Shared {  // at kOffMisc
     uint64_t full[12], empty[12];
     uint64_t sfull[2], pfull[2], pfree[2];
     uint64_t qfull, qempty, ofull, drain;
     uint32_t tmem;
-    int abort, last, unused;
+    int abort;
     unsigned long long bad_v;          // drafted slots with non-finite values, this segment
-    int tiles[kMaxLanes], lo[kMaxLanes], nodes[kMaxLanes], len[kMaxLanes], end[kMaxLanes];
-    int base[kMaxLanes + 1];           // first unit of each lane
-    int width;                         // CTAs that share a (lane, head), one per block of query rows
+    Lanes lanes;
     uint64_t vis[128];                 // drafted slots each column sees
     alignas(16) float neg_m[128];      // each column's reference, negated
     float inv[128];                    // 1 / sum
@@ -120,7 +126,7 @@ struct AttnParams {
     nvfp4_attn_args a;
     float* part_o;       // [ctas][2][N][D]
     float2* part_ml;     // [ctas][2][N]
-    unsigned* counters;  // [ctas]
+    int ctas;            // of the attention kernel
     int min_tiles;       // tiles a CTA takes at least (but for the last ones)
     int per_block;       // rows of a lane per block: as many whole rows (of G columns) as fit N
     int q_box;           // rows a copy of Q brings (at most per_block)
@@ -331,7 +337,62 @@ struct Segment {
     int first;        // the pair's first unit
 };
 
-__device__ __forceinline__ Segment segment_at(const Shared& s, int lanes, int u, int u1)
+__device__ __forceinline__ int range_begin(int units, int groups, int g) { return (int)((int64_t)units * g / groups); }
+__device__ __forceinline__ int range_owner(int units, int groups, int u)
+{
+    return (int)((((int64_t)u + 1) * groups - 1) / units);
+}
+
+// The lanes' rows, lengths and tiles, and the groups, for a whole CTA (two
+// barriers inside; the caller's own follows).
+__device__ __forceinline__ void plan_lanes(const AttnParams& p, Lanes& s, int tid, bool tell)
+{
+    const nvfp4_cache& c = p.c;
+    if (tid < kMaxLanes) {
+        int lo = 0, hi = 0, len = 0, end = 0, tiles = 0;
+        if (tid < c.lanes) {
+            lane_rows(p.a.row_start, tid, p.a.rows, lo, hi);
+            const int64_t cap = (int64_t)c.max_pages * c.page_size;
+            const int64_t n = max(c.len[tid], 0);
+            len = (int)(n < cap ? n : cap);
+            const int64_t e = n + (hi - lo);
+            end = (int)(e < cap ? e : cap);
+            if (hi > lo) {
+                tiles = (end + kTile - 1) / kTile;
+                if (e > cap && tell) atomicOr(&g_attn_status, kBadPage);
+            }
+        }
+        s.lo[tid] = lo;
+        s.nodes[tid] = hi - lo;
+        s.len[tid] = len;
+        s.end[tid] = end;
+        s.tiles[tid] = tiles;
+    }
+    __syncthreads();
+    if (tid < 32) {
+        // prefix sums of units and the widest lane, two lanes per thread
+        const int lane = tid;
+        const int x0 = s.tiles[2 * lane] * c.kv_heads, x1 = s.tiles[2 * lane + 1] * c.kv_heads;
+        int incl = x0 + x1, most = max(s.nodes[2 * lane], s.nodes[2 * lane + 1]);
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+            most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
+        }
+        s.base[2 * lane] = incl - x0 - x1;
+        s.base[2 * lane + 1] = incl - x1;
+        if (lane == 31) {
+            s.base[kMaxLanes] = incl;
+            const int width = max(1, (most + p.per_block - 1) / p.per_block);
+            s.width = width;
+            s.groups = min(p.ctas / width, (incl + p.min_tiles - 1) / p.min_tiles);
+        }
+    }
+    __syncthreads();
+}
+
+__device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, int u1)
 {
     Segment g;
     int b = 0;
@@ -442,98 +503,6 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
     any_of(bar, 128, false);
 }
 
-// ------------------------------------------------------------------- joins
-
-// The parts of a (lane, head) pair's columns, in CTA order: part 0 at row
-// `first` of the workspace, part q > 0 at rest + q step.
-template <int D, int N>
-__device__ __forceinline__ void join_parts(const AttnParams& p, Shared& s, uint8_t* space, int tid, int rows, int np,
-                                        int64_t first, int64_t rest, int64_t step)
-{
-    using L = Plan<D, N>;
-    constexpr int kAllBar = 5, kSoftThreads = L::kSoftThreads;
-    const nvfp4_attn_args& a = p.a;
-    // Maxima and sums of all parts come first, all loads at once, into the (now
-    // idle) space of P; then the weights.
-    float2* ml = reinterpret_cast<float2*>(space);
-    const bool fits = np * rows * 8 <= L::kPBufs * L::kPBytes;
-    if (fits)
-        for (int i = tid; i < np * rows; i += kSoftThreads) {
-            const int q = i / rows, col = i - q * rows;
-            ml[i] = __ldcg(&p.part_ml[(q ? rest + q * step : first) + col]);
-        }
-    any_of(kAllBar, kSoftThreads, false);
-    auto part_of = [&](int q, int col) {
-        return fits ? ml[q * rows + col] : __ldcg(&p.part_ml[(q ? rest + q * step : first) + col]);
-    };
-    if (tid < rows) {
-        float top = kUnseen, sum = 0.f;
-#pragma unroll 8
-        for (int q = 0; q < np; ++q) top = fmaxf(top, part_of(q, tid).x);
-#pragma unroll 8
-        for (int q = 0; q < np; ++q) {
-            const float2 v = part_of(q, tid);
-            const float w = v.x == top ? 1.f : fast_exp2(v.x - top);
-            sum += v.y * w;
-            if (fits) ml[q * rows + tid].x = w;
-        }
-        s.neg_m[tid] = -top;
-        s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
-        if (a.lse) a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-    }
-    any_of(kAllBar, kSoftThreads, false);
-    constexpr int kQuads = D / 4, kOnce = 4;  // float4 of a row; how many a thread sums at a time
-    for (int i0 = tid; i0 < rows * kQuads; i0 += kOnce * kSoftThreads) {
-        float4 acc[kOnce];
-#pragma unroll
-        for (int z = 0; z < kOnce; ++z) acc[z] = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 2
-        for (int q = 0; q < np; ++q) {
-            const float4* src = reinterpret_cast<const float4*>(p.part_o + (q ? rest + q * step : first) * D);
-            float4 v[kOnce];
-#pragma unroll
-            for (int z = 0; z < kOnce; ++z) {
-                const int i = i0 + z * kSoftThreads;
-                if (i < rows * kQuads) v[z] = __ldcg(src + i);
-            }
-#pragma unroll
-            for (int z = 0; z < kOnce; ++z) {
-                const int i = i0 + z * kSoftThreads;
-                if (i < rows * kQuads) {
-                    const int col = i / kQuads;
-                    float w = part_of(q, col).x;
-                    if (!fits) w = w == -s.neg_m[col] ? 1.f : fast_exp2(w + s.neg_m[col]);
-                    acc[z].x += w * v[z].x;
-                    acc[z].y += w * v[z].y;
-                    acc[z].z += w * v[z].z;
-                    acc[z].w += w * v[z].w;
-                }
-            }
-        }
-#pragma unroll
-        for (int z = 0; z < kOnce; ++z) {
-            const int i = i0 + z * kSoftThreads;
-            if (i < rows * kQuads) {
-                const int col = i / kQuads, d = i % kQuads * 4;
-                const float inv = s.inv[col];
-                __nv_bfloat162 h0 = __floats2bfloat162_rn(acc[z].x * inv, acc[z].y * inv);
-                __nv_bfloat162 h1 = __floats2bfloat162_rn(acc[z].z * inv, acc[z].w * inv);
-                *reinterpret_cast<uint2*>((uint16_t*)a.out + s.off[col] + d) =
-                    make_uint2(*reinterpret_cast<uint32_t*>(&h0), *reinterpret_cast<uint32_t*>(&h1));
-            }
-        }
-    }
-}
-
-// With 128 columns a call of its own: in line it would cost the softmax loop
-// spills, which go to L2 here (the plans leave L1 no room).
-template <int D, int N>
-__device__ __noinline__ void join_parts_apart(const AttnParams& p, Shared& s, uint8_t* space, int tid, int rows, int np,
-                                              int64_t first, int64_t rest, int64_t step)
-{
-    join_parts<D, N>(p, s, space, tid, rows, np, first, rest, step);
-}
-
 // ---------------------------------------------------------------- the kernel
 
 template <int D, int N>
@@ -591,55 +560,16 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         *reinterpret_cast<uint4*>(sm + L::kOffQ + i * 16) = make_uint4(0, 0, 0, 0);
     fence_async();
     pdl_begin();
-    // the lanes: rows, lengths, tiles
-    if (tid < kMaxLanes) {
-        int lo = 0, hi = 0, len = 0, end = 0, tiles = 0;
-        if (tid < c.lanes) {
-            lane_rows(a.row_start, tid, a.rows, lo, hi);
-            const int64_t cap = (int64_t)c.max_pages << shift;
-            const int64_t n = max(c.len[tid], 0);
-            len = (int)(n < cap ? n : cap);
-            const int64_t e = n + (hi - lo);
-            end = (int)(e < cap ? e : cap);
-            if (hi > lo) {
-                tiles = (end + kTile - 1) / kTile;
-                if (e > cap && blockIdx.x == 0) atomicOr(&g_attn_status, kBadPage);
-            }
-        }
-        s.lo[tid] = lo;
-        s.nodes[tid] = hi - lo;
-        s.len[tid] = len;
-        s.end[tid] = end;
-        s.tiles[tid] = tiles;
-    }
-    __syncthreads();
-    if (warp == 0) {
-        // prefix sums of units and the widest lane, two lanes per thread
-        const int x0 = s.tiles[2 * lane] * c.kv_heads, x1 = s.tiles[2 * lane + 1] * c.kv_heads;
-        int incl = x0 + x1, most = max(s.nodes[2 * lane], s.nodes[2 * lane + 1]);
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
-        }
-        s.base[2 * lane] = incl - x0 - x1;
-        s.base[2 * lane + 1] = incl - x1;
-        if (lane == 31) s.base[kMaxLanes] = incl;
-        if (lane == 0) s.width = max(1, (most + p.per_block - 1) / p.per_block);
-    }
+    plan_lanes(p, s.lanes, tid, blockIdx.x == 0);
     fence_after();
     __syncthreads();
     const uint32_t tmem = s.tmem;
     const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
     // this CTA's range and its block of query rows
-    const int units = s.base[kMaxLanes], width = s.width;
-    int groups = gridDim.x / width;
-    if (groups > (units + p.min_tiles - 1) / p.min_tiles) groups = (units + p.min_tiles - 1) / p.min_tiles;
+    const int units = s.lanes.base[kMaxLanes], width = s.lanes.width, groups = s.lanes.groups;
     const int group = blockIdx.x / width, blk = blockIdx.x % width;
-    const bool idle = units == 0 || group >= groups;
-    const int u0 = idle ? 0 : (int)((int64_t)units * group / groups);
-    const int u1 = idle ? 0 : (int)((int64_t)units * (group + 1) / groups);
+    const bool idle = group >= groups;
+    const int u0 = idle ? 0 : range_begin(units, groups, group), u1 = idle ? 0 : range_begin(units, groups, group + 1);
 
     if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRest));
     if (warp == kLoadWarp) {
@@ -650,12 +580,12 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         const int box = min(c.page_size, kTile);         // slots per copy
         const int pieces = kTile / box;                  // copies per atom of a tile
         for (int u = u0; ok && u < u1;) {
-            const Segment g = segment_at(s, c.lanes, u, u1);
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.nodes[g.b]) continue;
+            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
-            const int end = s.end[g.b];
+            const int end = s.lanes.end[g.b];
             // lane i < pieces holds the page of piece i; one tile ahead for K
             auto page_of = [&](int t) {
                 const int slot = (g.t0 + t) * kTile + lane * box;
@@ -703,15 +633,15 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         int seg = 0;
         bool ok = true;
         for (int u = u0; ok && u < u1;) {
-            const Segment g = segment_at(s, c.lanes, u, u1);
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.nodes[g.b]) continue;
+            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             if (seg > 0) ok = waitw(smem_addr(&s.qempty), (seg - 1) & 1, abort);
             if (ok && lane == 0) {
                 const uint32_t bar = smem_addr(&s.qfull);
                 mbar_expect_tx(bar, (uint32_t)(p.q_box * G * D * 2));
                 for (int x = 0; x < D / 64; ++x)
-                    tma_rows(qbuf + x * N * 128, &map_q, x * 64, g.h * G, s.lo[g.b] + blk * p.per_block, bar);
+                    tma_rows(qbuf + x * N * 128, &map_q, x * 64, g.h * G, s.lanes.lo[g.b] + blk * p.per_block, bar);
             }
             __syncwarp();
             ++seg;
@@ -729,9 +659,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         int done = 0;  // tiles of earlier segments
         bool ok = true;
         for (int u = u0; ok && u < u1;) {
-            const Segment g = segment_at(s, c.lanes, u, u1);
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.nodes[g.b]) continue;
+            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
             fence_after();
@@ -799,19 +729,19 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         int seg = 0, done = 0, idx = 0;
         bool fail = false;
         for (int u = u0; u < u1;) {
-            const Segment g = segment_at(s, c.lanes, u, u1);
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.nodes[g.b]) continue;
+            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
-            const int len = s.len[g.b], end = s.end[g.b], lo = s.lo[g.b];
-            const int rows = min(p.per_block, s.nodes[g.b] - blk * p.per_block) * G;  // columns in use
+            const int len = s.lanes.len[g.b], end = s.lanes.end[g.b], lo = s.lanes.lo[g.b];
+            const int rows = min(p.per_block, s.lanes.nodes[g.b] - blk * p.per_block) * G;  // columns in use
             const int32_t* trow = c.table + (int64_t)g.b * c.max_pages;
             int pg = g.t0 * kTile + srow < end ? trow[(g.t0 * kTile + srow) >> shift] : -1;
             // column j of the block is row lo + i, i = blk per_block + j / G, head h G + j % G
             if (tid < N) {
                 uint64_t w = 0;
                 if (tid < rows) {
-                    const int i = blk * p.per_block + tid / G, head = g.h * G + tid % G, T = s.nodes[g.b];
+                    const int i = blk * p.per_block + tid / G, head = g.h * G + tid % G, T = s.lanes.nodes[g.b];
                     w = a.mask ? a.mask[lo + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
                     if (T < 64) w &= (1ull << T) - 1;
                     s.off[tid] = (int64_t)(lo + i) * a.ldo + (int64_t)head * D;
@@ -936,7 +866,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fail = true;
                 break;
             }
-            const bool whole = g.t0 == 0 && g.t1 == s.tiles[g.b];
+            const bool whole = g.t0 == 0 && g.t1 == s.lanes.tiles[g.b];
             const int pslot = g.first <= u0 ? 0 : 1;
             const int64_t part = (int64_t)blockIdx.x * 2 + pslot;
             if (tid < N) {
@@ -990,25 +920,6 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 }
             }
             fence_before();
-            if (!whole) {
-                // the pair's CTAs: those of the groups that hold its first to its last unit
-                const int last_u = g.first + s.tiles[g.b] - 1;
-                const int glo = (int)((((int64_t)g.first + 1) * groups - 1) / units);
-                const int ghi = (int)((((int64_t)last_u + 1) * groups - 1) / units);
-                __threadfence();
-                any_of(kAllBar, kSoftThreads, false);
-                if (tid == 0) s.last = count_in(p.counters + glo * width + blk) == (unsigned)(ghi - glo);
-                any_of(kAllBar, kSoftThreads, false);
-                if (s.last) {
-                    const int lo_slot = (int)((int64_t)units * glo / groups) >= g.first ? 0 : 1;
-                    const int64_t rest = (int64_t)(glo * width + blk) * 2 * N, step = (int64_t)width * 2 * N;
-                    if constexpr (N == 128)
-                        join_parts_apart<D, N>(p, s, sm + L::kOffP, tid, rows, ghi - glo + 1, rest + lo_slot * N, rest, step);
-                    else
-                        join_parts<D, N>(p, s, sm + L::kOffP, tid, rows, ghi - glo + 1, rest + lo_slot * N, rest, step);
-                    if (tid == 0) p.counters[glo * width + blk] = 0u;
-                }
-            }
             any_of(kAllBar, kSoftThreads, false);  // the tables of this segment are done with
             done += n;
             idx += 2 * n * L::kPer;
@@ -1022,6 +933,87 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         fence_after();
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
     }
+}
+
+// ------------------------------------------------------------------- joins
+
+// The parts of (lane, head) pairs that were cut between CTAs, joined in CTA
+// order: a warp per (row, head), all warps of the GPU at once.  (The last CTA
+// of a pair joining it in the first kernel took 20 us and more for twelve parts
+// of 48 x 256: one SM's loads.)
+template <int D, int N>
+__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p)
+{
+    __shared__ Lanes s;
+    const nvfp4_attn_args& a = p.a;
+    pdl_begin();
+    plan_lanes(p, s, threadIdx.x, false);
+    const int lane = threadIdx.x & 31, id = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
+    const int r = id / a.q_heads, head = id - r * a.q_heads, G = a.q_heads / p.c.kv_heads;
+    if (r >= a.rows) return;
+    // the row's lane: the one whose rows hold it (two lanes per thread)
+    const int b0 = 2 * lane, b1 = 2 * lane + 1;
+    const unsigned h0 = __ballot_sync(0xffffffffu, r >= s.lo[b0] && r < s.lo[b0] + s.nodes[b0]);
+    const unsigned h1 = __ballot_sync(0xffffffffu, r >= s.lo[b1] && r < s.lo[b1] + s.nodes[b1]);
+    if (!(h0 | h1)) return;
+    const int b = h0 ? 2 * (__ffs(h0) - 1) : 2 * (__ffs(h1) - 1) + 1;
+    const int i = r - s.lo[b], blk = i / p.per_block, col = (i - blk * p.per_block) * G + head % G;
+    const int units = s.base[kMaxLanes], first = s.base[b] + head / G * s.tiles[b], last = first + s.tiles[b] - 1;
+    const int glo = range_owner(units, s.groups, first), ghi = range_owner(units, s.groups, last);
+    if (glo == ghi) return;  // not cut: written by the attention kernel
+    // part q of the pair: CTA (glo + q) width + blk, its last segment for q = 0 (unless that is its only one)
+    const int np = ghi - glo + 1, lo_slot = range_begin(units, s.groups, glo) >= first ? 0 : 1;
+    const int64_t rest = ((int64_t)(glo * s.width + blk) * 2) * N + col, step = (int64_t)s.width * 2 * N;
+    auto at = [&](int q) { return q ? rest + q * step : rest + lo_slot * N; };
+    constexpr int kPer = D / 32;  // values per lane
+    float top = kUnseen;
+    for (int q = lane; q < np; q += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(q)]).x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.f, acc[kPer];
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    for (int q0 = 0; q0 < np; q0 += 32) {
+        float w = 0.f;
+        if (q0 + lane < np) {
+            const float2 ml = __ldcg(&p.part_ml[at(q0 + lane)]);
+            w = ml.x == top ? 1.f : fast_exp2(ml.x - top);
+            sum += ml.y * w;
+        }
+        const int n = min(32, np - q0);
+#pragma unroll 8
+        for (int j = 0; j < n; ++j) {
+            const float wj = __shfl_sync(0xffffffffu, w, j);
+            const float* src = p.part_o + at(q0 + j) * D;
+            if constexpr (kPer == 2) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(src) + lane);
+                acc[0] += wj * v.x;
+                acc[1] += wj * v.y;
+            } else {
+#pragma unroll
+                for (int e = 0; e < kPer; e += 4) {
+                    const float4 v = __ldcg(reinterpret_cast<const float4*>(src) + lane + 8 * e);
+                    acc[e] += wj * v.x;
+                    acc[e + 1] += wj * v.y;
+                    acc[e + 2] += wj * v.z;
+                    acc[e + 3] += wj * v.w;
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    uint32_t* out = reinterpret_cast<uint32_t*>((uint16_t*)a.out + (int64_t)r * a.ldo + (int64_t)head * D);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+        const __nv_bfloat162 h = __floats2bfloat162_rn(acc[e] * inv, acc[e + 1] * inv);
+        // lane's values: 2 from 2 lane on (64), else 4 from 4 lane + 128 (e / 4) on
+        const int d = kPer == 2 ? 2 * lane : 4 * lane + 32 * (e & ~3) + (e & 2);
+        out[d / 2] = *reinterpret_cast<const uint32_t*>(&h);
+    }
+    if (lane == 0 && a.lse)
+        a.lse[(int64_t)r * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // ------------------------------------------------------------------- host
@@ -1082,20 +1074,19 @@ int block_rows(int max_nodes, int rows, int g)
 }
 
 struct Workspace {
-    size_t o, ml, bytes;
+    size_t o, bytes;  // (m, l) pairs first
 };
 Workspace workspace(int head_dim, int sms)
 {
-    // two partials per CTA at the widest block; the counters first
+    // two parts per CTA at the widest block
     Workspace w;
-    w.ml = ((size_t)sms * sizeof(unsigned) + 255) / 256 * 256;
-    w.o = w.ml + (size_t)sms * 2 * 128 * sizeof(float2);
+    w.o = (size_t)sms * 2 * 128 * sizeof(float2);
     w.bytes = w.o + (size_t)sms * 2 * 128 * head_dim * sizeof(float);
     return w;
 }
 
 template <int D, int N>
-int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, int sms,
+int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
                    cudaStream_t stream)
 {
     using L = Plan<D, N>;
@@ -1109,19 +1100,24 @@ int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap
         NVFP4_CUDA_TRY(cudaFuncSetAttribute(attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
         ready.fetch_or(1ull << dev);
     }
-    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)sms), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
+    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)p.ctas), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
+    // a table of one tile cannot be cut
+    if ((int64_t)p.c.max_pages * p.c.page_size > kTile) {
+        const unsigned grid = (unsigned)((p.a.rows * p.a.q_heads + 7) / 8);
+        NVFP4_CUDA_TRY(launch_pdl(attn_join_kernel<D, N>, dim3(grid), dim3(256), 0, stream, p));
+    }
     return NVFP4_OK;
 }
 
 template <int D>
-int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq, int sms,
+int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensorMap& mv, const CUtensorMap& mq,
                cudaStream_t stream)
 {
     switch (n) {
-    case 16: return launch_variant<D, 16>(p, mk, mv, mq, sms, stream);
-    case 32: return launch_variant<D, 32>(p, mk, mv, mq, sms, stream);
-    case 64: return launch_variant<D, 64>(p, mk, mv, mq, sms, stream);
-    default: return launch_variant<D, 128>(p, mk, mv, mq, sms, stream);
+    case 16: return launch_variant<D, 16>(p, mk, mv, mq, stream);
+    case 32: return launch_variant<D, 32>(p, mk, mv, mq, stream);
+    case 64: return launch_variant<D, 64>(p, mk, mv, mq, stream);
+    default: return launch_variant<D, 128>(p, mk, mv, mq, stream);
     }
 }
 
@@ -1168,11 +1164,11 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     int sms = 0;
     int st = sm_count(&sms);
     if (st != NVFP4_OK) return st;
+    p.ctas = sms;
     const Workspace w = workspace(p.c.head_dim, sms);
     if (a->workspace_bytes < w.bytes) return NVFP4_ERR_SCRATCH;
     uint8_t* base = (uint8_t*)a->workspace;
-    p.counters = (unsigned*)base;
-    p.part_ml = (float2*)(base + w.ml);
+    p.part_ml = (float2*)base;
     p.part_o = (float*)(base + w.o);
     EncodeFn encode = nullptr;
     st = encoder(&encode);
@@ -1188,9 +1184,9 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     st = query_map(encode, *a, g, p.q_box, &mq);
     if (st != NVFP4_OK) return st;
     if (sms < NVFP4_ATTN_MAX_ROWS) return fail_cuda(cudaErrorInvalidDevice);
-    return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, mq, sms, stream)
-           : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, mq, sms, stream)
-                                 : launch_dim<256>(n, p, mk, mv, mq, sms, stream);
+    return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, mq, stream)
+           : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, mq, stream)
+                                 : launch_dim<256>(n, p, mk, mv, mq, stream);
 }
 
 }  // namespace nvfp4
