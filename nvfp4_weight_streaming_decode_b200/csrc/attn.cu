@@ -72,7 +72,7 @@ struct Plan {
     static constexpr int kAtoms = D >= 128 ? 2 : 1;          // atoms per ring entry
     static constexpr int kEntry = kAtoms * kTile * 128;      // bytes
     static constexpr int kPer = D > 128 ? 2 : 1;             // entries per tile of K (or V)
-    static constexpr int kPBufs = N == 128 ? 1 : 2;
+    static constexpr int kPBufs = N == 128 && D == 256 ? 1 : 2;
     static constexpr int kPBytes = kTile * N * 2;
     static constexpr int kQBytes = N * D * 2;
     static constexpr int kBudget = 226 * 1024 - 8192;        // what is left holds barriers and the lane tables
@@ -330,11 +330,16 @@ __device__ __forceinline__ float max3(float a, float b, float c)
 // ------------------------------------------------------------- the schedule
 
 // Units are (lane, cached head, tile), lane by lane; a group of `width` CTAs
-// (one per block of query rows) takes a contiguous range of them.
+// (one per block of query rows) takes a contiguous range of them.  Each pair
+// begins with kStart units without a tile, about what starting and ending a
+// pair costs a CTA (with 0 the CTAs that got a border ran 10 % longer).
+constexpr int kStart = 4;
+
 struct Segment {
     int b, h;         // lane and cached head
     int t0, t1;       // tiles
     int first;        // the pair's first unit
+    int next;         // the unit after the segment
 };
 
 __device__ __forceinline__ int range_begin(int units, int groups, int g) { return (int)((int64_t)units * g / groups); }
@@ -372,7 +377,8 @@ __device__ __forceinline__ void plan_lanes(const AttnParams& p, Lanes& s, int ti
     if (tid < 32) {
         // prefix sums of units and the widest lane, two lanes per thread
         const int lane = tid;
-        const int x0 = s.tiles[2 * lane] * c.kv_heads, x1 = s.tiles[2 * lane + 1] * c.kv_heads;
+        const int n0 = s.tiles[2 * lane], n1 = s.tiles[2 * lane + 1];
+        const int x0 = n0 ? (n0 + kStart) * c.kv_heads : 0, x1 = n1 ? (n1 + kStart) * c.kv_heads : 0;
         int incl = x0 + x1, most = max(s.nodes[2 * lane], s.nodes[2 * lane + 1]);
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
@@ -397,12 +403,13 @@ __device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, 
     Segment g;
     int b = 0;
     while (b + 1 < lanes && s.base[b + 1] <= u) ++b;
-    const int r = u - s.base[b], n = s.tiles[b];
+    const int r = u - s.base[b], n = kStart + s.tiles[b];
     g.b = b;
     g.h = r / n;
-    g.t0 = r - g.h * n;
     g.first = s.base[b] + g.h * n;
-    g.t1 = min(n, g.t0 + (u1 - u));
+    g.next = min(g.first + n, u1);
+    g.t0 = max(u - g.first - kStart, 0);
+    g.t1 = g.next - g.first - kStart;  // <= t0: nothing but (a part of) the start
     return g;
 }
 
@@ -431,6 +438,28 @@ __device__ __forceinline__ void read_scores(uint32_t at, float (&x)[C], bool pla
         for (int i = 0; i < C; ++i)
             if (!all && !(vis[i] & bit)) x[i] = -INFINITY;
     }
+}
+
+// C log2 scores become weights, which also go to this slot's row of P, rounded
+// to bf16; returns the largest score.
+template <int C>
+__device__ __forceinline__ float weigh(float (&x)[C], uint8_t* prow)
+{
+    float over = fmaxf(x[0], x[1]);
+#pragma unroll
+    for (int i = 0; i < C; i += 8) {
+        uint32_t w[4];
+#pragma unroll
+        for (int j = 0; j < 8; j += 2) {
+            over = max3(over, x[i + j], x[i + j + 1]);
+            x[i + j] = fast_exp2(x[i + j]);
+            x[i + j + 1] = fast_exp2(x[i + j + 1]);
+            const __nv_bfloat162 h = __floats2bfloat162_rn(x[i + j], x[i + j + 1]);
+            w[j / 2] = *reinterpret_cast<const uint32_t*>(&h);
+        }
+        *reinterpret_cast<uint4*>(prow + (i >> 3) * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    return over;
 }
 
 // ------------------------------------------------------------ new references
@@ -559,7 +588,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     for (int i = tid; i < L::kQBytes / 16; i += L::kThreads)
         *reinterpret_cast<uint4*>(sm + L::kOffQ + i * 16) = make_uint4(0, 0, 0, 0);
     fence_async();
-    pdl_begin();
+    // The join may start once what came before this kernel is complete: it then
+    // reads row ranges and lengths while this one runs out.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan_lanes(p, s.lanes, tid, blockIdx.x == 0);
     fence_after();
     __syncthreads();
@@ -581,8 +613,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         const int pieces = kTile / box;                  // copies per atom of a tile
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
             const int end = s.lanes.end[g.b];
@@ -634,8 +666,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         bool ok = true;
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             if (seg > 0) ok = waitw(smem_addr(&s.qempty), (seg - 1) & 1, abort);
             if (ok && lane == 0) {
                 const uint32_t bar = smem_addr(&s.qfull);
@@ -660,8 +692,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         bool ok = true;
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
             fence_after();
@@ -730,8 +762,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
         bool fail = false;
         for (int u = u0; u < u1;) {
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u += g.t1 - g.t0;
-            if (blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
             const int n = g.t1 - g.t0;
             const int len = s.lanes.len[g.b], end = s.lanes.end[g.b], lo = s.lanes.lo[g.b];
             const int rows = min(p.per_block, s.lanes.nodes[g.b] - blk * p.per_block) * G;  // columns in use
@@ -771,10 +803,13 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fence_after();
                 float x[C];
                 read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
-                // over the reference by more than the headroom?
-                float over = fmaxf(x[0], x[1]);
-#pragma unroll
-                for (int i = 2; i < C; i += 2) over = max3(over, x[i], x[i + 1]);
+                // Two buffers of P: S of this tile was issued after O of the tile before the
+                // last, so once S is there the weights of that tile are done with.
+                if (L::kPBufs == 1 && T > 0) fail = fail || !waitw(smem_addr(&s.pfree[0]), (T - 1) & 1, abort);
+                uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
+                // The weights are formed before it is known whether the references hold
+                // (the maxima hide behind the exponentials); if not, again.
+                const float over = weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
                 if (any_of(bar, 128, over > kHeadroom || fail)) {
                     if (any_of(bar, 128, fail)) {
                         if (lane == 0) give_up(abort);
@@ -784,25 +819,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                     rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
                                smem_addr(&s.pfree[(T + L::kPBufs - 1) % L::kPBufs]), ((T - 1) / L::kPBufs) & 1, abort, fail);
                     read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
+                    weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
                 }
-                // (two buffers: S of this tile was issued after O of the tile before the
-                // last, so once S is there the weights of that tile are done with)
-                if (L::kPBufs == 1 && T > 0)
-                    fail = fail || !waitw(smem_addr(&s.pfree[pb]), ((T / L::kPBufs) - 1) & 1, abort);
-                // weights
-                uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
 #pragma unroll
-                for (int i = 0; i < C; i += 8) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const float y0 = fast_exp2(x[i + 2 * j]), y1 = fast_exp2(x[i + 2 * j + 1]);
-                        l[i / 2 + j] = add2(l[i / 2 + j], pair(y0, y1));
-                        const __nv_bfloat162 h = __floats2bfloat162_rn(y0, y1);
-                        w[j] = *reinterpret_cast<const uint32_t*>(&h);
-                    }
-                    *reinterpret_cast<uint4*>(prow + ((c0 + i) >> 3) * (kTile * 16)) = make_uint4(w[0], w[1], w[2], w[3]);
-                }
+                for (int i = 0; i < C / 2; ++i) l[i] = add2(l[i], pair(x[2 * i], x[2 * i + 1]));
                 if (!plain) {
                     // V rows that are nobody's slot: zero; of drafted slots: their non-finite values
                     for (int e = 0; e < L::kPer; ++e) {
@@ -946,20 +966,25 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
 {
     __shared__ Lanes s;
     const nvfp4_attn_args& a = p.a;
-    pdl_begin();
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     plan_lanes(p, s, threadIdx.x, false);
     const int lane = threadIdx.x & 31, id = (int)blockIdx.x * 8 + (threadIdx.x >> 5);
     const int r = id / a.q_heads, head = id - r * a.q_heads, G = a.q_heads / p.c.kv_heads;
-    if (r >= a.rows) return;
+    if (r >= a.rows) {
+        asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
     // the row's lane: the one whose rows hold it (two lanes per thread)
     const int b0 = 2 * lane, b1 = 2 * lane + 1;
     const unsigned h0 = __ballot_sync(0xffffffffu, r >= s.lo[b0] && r < s.lo[b0] + s.nodes[b0]);
     const unsigned h1 = __ballot_sync(0xffffffffu, r >= s.lo[b1] && r < s.lo[b1] + s.nodes[b1]);
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the parts are there
     if (!(h0 | h1)) return;
     const int b = h0 ? 2 * (__ffs(h0) - 1) : 2 * (__ffs(h1) - 1) + 1;
     const int i = r - s.lo[b], blk = i / p.per_block, col = (i - blk * p.per_block) * G + head % G;
-    const int units = s.base[kMaxLanes], first = s.base[b] + head / G * s.tiles[b], last = first + s.tiles[b] - 1;
-    const int glo = range_owner(units, s.groups, first), ghi = range_owner(units, s.groups, last);
+    const int units = s.base[kMaxLanes], first = s.base[b] + head / G * (kStart + s.tiles[b]);
+    const int glo = range_owner(units, s.groups, first + kStart),
+              ghi = range_owner(units, s.groups, first + kStart + s.tiles[b] - 1);
     if (glo == ghi) return;  // not cut: written by the attention kernel
     // part q of the pair: CTA (glo + q) width + blk, its last segment for q = 0 (unless that is its only one)
     const int np = ghi - glo + 1, lo_slot = range_begin(units, s.groups, glo) >= first ? 0 : 1;
