@@ -162,10 +162,11 @@ NVFP4_API int nvfp4_gemm_gateup_silu(const void* X, int M,
                            void* H, int64_t Nff, int64_t K, nvfp4_stream_t stream);
 
 /* One node of a decode round. */
-enum { NVFP4_DESC_GEMM = 0, NVFP4_DESC_GATEUP_SILU = 1 };
+enum { NVFP4_DESC_GEMM = 0, NVFP4_DESC_GATEUP_SILU = 1, NVFP4_DESC_ROPE_APPEND = 2, NVFP4_DESC_ATTN_TREE = 3 };
 typedef struct {
-    int kind;              /* NVFP4_DESC_GEMM or NVFP4_DESC_GATEUP_SILU */
-    const void* X;         /* bf16 [M][K], rows for M = 8 must be allocated */
+    int kind;              /* NVFP4_DESC_* */
+    const void* X;         /* bf16 [M][K], rows for M = 8 must be allocated; for ROPE_APPEND and
+                              ATTN_TREE a host nvfp4_rope_args / nvfp4_attn_args (the other fields unused) */
     const uint8_t* wq;     /* device-layout planes (gate for GATEUP_SILU) */
     const uint8_t* ws;
     float gscale;
@@ -184,6 +185,14 @@ typedef struct {
  * round": per-width CUDA graphs, widths 1..8).  The descriptor array is
  * copied; the buffers it names must outlive the round.  Allocates the graphs
  * and the per-device workspace.  Synchronous; *out is a host pointer.
+ *
+ * Nodes between the GEMMs: NVFP4_DESC_ROPE_APPEND and NVFP4_DESC_ATTN_TREE run
+ * nvfp4_rope_append and nvfp4_attn_tree with one row per lane, as many as the
+ * round's width: their arguments (copied, the cache description too) have
+ * row_start NULL and room for 8 rows, and a cache of at least 8 lanes, else
+ * NVFP4_ERR_ARG or NVFP4_ERR_M; `rows` in them is not looked at.  Lengths are
+ * read when the round runs and not changed: nvfp4_cache_reserve before a round,
+ * nvfp4_cache_compact after it.  NVFP4_ROUND_CHAIN only.
  */
 NVFP4_API int nvfp4_round_create(const nvfp4_gemm_desc* descs, int n, nvfp4_round** out);
 
@@ -442,7 +451,7 @@ NVFP4_API int nvfp4_cache_trim(const nvfp4_cache* cache, const int32_t* new_len,
  * inv_freq: device double [rot_dim / 2].  The angle is formed and reduced in
  * 64 bits, so far positions keep their phase; each output is rounded once.
  *
- * Limits: 1 <= rows (NVFP4_ERR_M), 0 <= layer < layers, 1 <= axes <= 4,
+ * Limits: 1 <= rows <= 65535 (NVFP4_ERR_M), 0 <= layer < layers, 1 <= axes <= 4,
  * q_heads a multiple of kv_heads, rot_dim <= head_dim, ldy >= the row, % 4 ==
  * 0, ldq >= q_heads * head_dim, % 8 == 0, ldp >= rows (NVFP4_ERR_SHAPE); y and q
  * 16-byte aligned, inv_freq 8-byte, the others 4-byte (NVFP4_ERR_ALIGN).
@@ -464,8 +473,8 @@ typedef struct {
 NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stream);
 
 /*
- * Attention of decode rows and drafted trees over the cache, one asynchronous
- * launch.  Rows and lanes as for nvfp4_rope_append; row r, the i-th of its
+ * Attention of decode rows and drafted trees over the cache, asynchronous (two
+ * launches; one where the table holds no more than 128 slots).  Rows and lanes as for nvfp4_rope_append; row r, the i-th of its
  * lane b of n rows, sees the lane's committed slots 0 .. len[b] - 1 and those
  * drafted slots len[b] + j, j < n, whose bit j is set in mask[r] (device u64
  * [rows]; a tree: itself and its ancestors).  mask NULL: j <= i, a chain; one
@@ -486,8 +495,8 @@ NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stre
  * least 1; it only chooses the tiling.  Results are the same from call to call.
  *
  * workspace: device, 16-byte aligned, of nvfp4_attn_tree_workspace() bytes
- * (else NVFP4_ERR_SCRATCH), zero-filled before its first use and then left to
- * the calls; calls that may overlap need one each.
+ * (else NVFP4_ERR_SCRATCH); nothing is kept in it from call to call, and calls
+ * that may overlap need one each.
  */
 #define NVFP4_ATTN_MAX_ROWS 64
 typedef struct {
@@ -530,8 +539,10 @@ NVFP4_API int nvfp4_attn_tree_workspace(int rows, int q_heads, int kv_heads, int
  * Limits: groups, beams >= 1, groups * beams <= NVFP4_TOPK_MAX_ROWS
  * (NVFP4_ERR_M); 1 <= V <= 2^20, ldv >= V, ldv % 4 == 0, and 0 <= eos < V
  * when finished is given (NVFP4_ERR_SHAPE); logits 16-byte aligned, others by
- * their type (NVFP4_ERR_ALIGN).  workspace: as for nvfp4_attn_tree, of
- * nvfp4_beam_select_workspace() bytes.
+ * their type (NVFP4_ERR_ALIGN).  workspace: device, 16-byte aligned, of
+ * nvfp4_beam_select_workspace() bytes (else NVFP4_ERR_SCRATCH), zero-filled
+ * before its first use and then left to the calls; calls that may overlap need
+ * one each.
  */
 NVFP4_API int nvfp4_beam_select(const float* logits, int groups, int beams, int64_t V, int64_t ldv,
                                 const float* scores, const uint8_t* finished, int eos, float* scores_out,

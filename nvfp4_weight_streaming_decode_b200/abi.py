@@ -34,6 +34,8 @@ NVFP4_ROUND_PERSISTENT = 0
 NVFP4_ROUND_CHAIN = 1
 NVFP4_DESC_GEMM = 0
 NVFP4_DESC_GATEUP_SILU = 1
+NVFP4_DESC_ROPE_APPEND = 2
+NVFP4_DESC_ATTN_TREE = 3
 NVFP4_TOPK_MAX_ROWS = 64
 NVFP4_TOPK_MAX_K = 64
 NVFP4_TOPK_MAX_V = 1 << 24
@@ -612,11 +614,11 @@ def _sm_count(device):
 
 
 def attn_tree_workspace(cache, rows, q_heads):
-    """A zero-filled workspace for attn_tree calls of these sizes (uint8)."""
+    """A workspace for attn_tree calls of these sizes (uint8)."""
     import torch
     st, n = nvfp4_attn_tree_workspace(rows, q_heads, cache.kv_heads, cache.head_dim, _sm_count(cache.device))
     check(st, "nvfp4_attn_tree_workspace")
-    return torch.zeros(n, dtype=torch.uint8, device=cache.device)
+    return torch.empty(n, dtype=torch.uint8, device=cache.device)
 
 
 def _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace):
@@ -792,3 +794,23 @@ def desc(kind, X, wq, ws, gscale, out, N, K, wq2=None, ws2=None, gscale2=0.0):
                          wq2.data_ptr() if wq2 is not None else None,
                          ws2.data_ptr() if ws2 is not None else None, float(gscale2),
                          out.data_ptr(), int(N), int(K))
+
+
+def _between(kind, record, *keep):
+    """A descriptor whose X is the record (kept alive with the tensors it names for as long as the descriptor)."""
+    buf = ctypes.create_string_buffer(record, len(record))
+    d = Nvfp4GemmDesc(kind, ctypes.addressof(buf))
+    d._keep = (buf, *keep)
+    return d
+
+
+def desc_rope(cache, layer, y, q_heads, inv_freq, positions, q, pair_axis=None, style=NVFP4_ROPE_HALVES):
+    """An Nvfp4GemmDesc of a round's rotary append (rope_append's arguments, one row per lane, 8 rows)."""
+    record, _ = _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, None, q)
+    return _between(NVFP4_DESC_ROPE_APPEND, record, cache, y, inv_freq, positions, q, pair_axis)
+
+
+def desc_attn(cache, layer, q, scale, out, workspace, lse=None):
+    """An Nvfp4GemmDesc of a round's attention (attn_tree's arguments, one row per lane, 8 rows)."""
+    record = _attn_record(cache, layer, q, scale, None, None, 1, out, False, lse, workspace)[0]
+    return _between(NVFP4_DESC_ATTN_TREE, record, cache, q, out, workspace, lse)

@@ -12,6 +12,12 @@
 
 #include "internal.h"
 
+struct Between {
+    nvfp4_cache cache;
+    nvfp4_rope_args rope;
+    nvfp4_attn_args attn;
+};
+
 struct nvfp4_round {
     int device;
     int n;
@@ -21,6 +27,7 @@ struct nvfp4_round {
     unsigned** d_arrive;      // persistent mode: per-chunk arrival counters (nodes + 1)
     float* d_temp;            // persistent mode: FP32 gate/up results of a fused node
     nvfp4_gemm_desc* descs;
+    struct Between* between;  // one per descriptor: the copied arguments of a node that is no GEMM
     cudaStream_t stream;
     cudaGraph_t graphs[nvfp4::kMaxM];
     cudaGraphExec_t execs[nvfp4::kMaxM];
@@ -47,6 +54,50 @@ nvfp4::GemmArgs args_of(const nvfp4_gemm_desc& d, int M)
     return a;
 }
 
+bool is_gemm(const nvfp4_gemm_desc& d) { return d.kind == NVFP4_DESC_GEMM || d.kind == NVFP4_DESC_GATEUP_SILU; }
+
+// The checks of a node that is no GEMM, at the widest round.
+int check_between(const nvfp4_gemm_desc& d)
+{
+    if (!d.X) return NVFP4_ERR_ARG;
+    if (d.kind == NVFP4_DESC_ROPE_APPEND) {
+        nvfp4_rope_args a = *(const nvfp4_rope_args*)d.X;
+        if (a.row_start) return NVFP4_ERR_ARG;
+        a.rows = nvfp4::kMaxM;
+        return nvfp4::validate_rope(&a);
+    }
+    nvfp4_attn_args a = *(const nvfp4_attn_args*)d.X;
+    if (a.row_start) return NVFP4_ERR_ARG;
+    a.rows = nvfp4::kMaxM;
+    return nvfp4::validate_attn(&a);
+}
+
+void copy_between(const nvfp4_gemm_desc& d, Between* b)
+{
+    if (d.kind == NVFP4_DESC_ROPE_APPEND) {
+        b->rope = *(const nvfp4_rope_args*)d.X;
+        b->cache = *b->rope.cache;
+        b->rope.cache = &b->cache;
+    } else {
+        b->attn = *(const nvfp4_attn_args*)d.X;
+        b->cache = *b->attn.cache;
+        b->attn.cache = &b->cache;
+        b->attn.max_nodes = 1;
+    }
+}
+
+int launch_between(const nvfp4_gemm_desc& d, const Between& b, int M, cudaStream_t stream)
+{
+    if (d.kind == NVFP4_DESC_ROPE_APPEND) {
+        nvfp4_rope_args a = b.rope;
+        a.rows = M;
+        return nvfp4::launch_rope(&a, stream);
+    }
+    nvfp4_attn_args a = b.attn;
+    a.rows = M;
+    return nvfp4::launch_attn(&a, stream);
+}
+
 void release(nvfp4_round* r)
 {
     if (!r) return;
@@ -63,6 +114,7 @@ void release(nvfp4_round* r)
     free(r->d_arrive);
     if (r->d_temp) cudaFree(r->d_temp);
     free(r->descs);
+    free(r->between);
     free(r);
 }
 
@@ -80,18 +132,22 @@ extern "C" int nvfp4_round_create_ex(const nvfp4_gemm_desc* descs, int n, int mo
     if (mode != NVFP4_ROUND_PERSISTENT && mode != NVFP4_ROUND_CHAIN) return NVFP4_ERR_ARG;
     *out = nullptr;
     for (int i = 0; i < n; ++i) {
-        const GemmArgs a = args_of(descs[i], kMaxM);
-        const int st = validate_gemm(a);
+        const bool between = descs[i].kind == NVFP4_DESC_ROPE_APPEND || descs[i].kind == NVFP4_DESC_ATTN_TREE;
+        if (between && mode != NVFP4_ROUND_CHAIN) return NVFP4_ERR_ARG;
+        const int st = between ? check_between(descs[i]) : validate_gemm(args_of(descs[i], kMaxM));
         if (st != NVFP4_OK) return st;
     }
     nvfp4_round* r = (nvfp4_round*)calloc(1, sizeof(nvfp4_round));
     if (!r) return NVFP4_ERR_ARG;
     r->descs = (nvfp4_gemm_desc*)malloc(sizeof(nvfp4_gemm_desc) * (size_t)n);
-    if (!r->descs) {
-        free(r);
+    r->between = (Between*)calloc((size_t)n, sizeof(Between));
+    if (!r->descs || !r->between) {
+        release(r);
         return NVFP4_ERR_ARG;
     }
     memcpy(r->descs, descs, sizeof(nvfp4_gemm_desc) * (size_t)n);
+    for (int i = 0; i < n; ++i)
+        if (!is_gemm(descs[i])) copy_between(descs[i], &r->between[i]);
     r->n = n;
     r->mode = mode;
     cudaError_t e = cudaGetDevice(&r->device);
@@ -156,7 +212,8 @@ extern "C" int nvfp4_round_create_ex(const nvfp4_gemm_desc* descs, int n, int mo
                 lst = round_persistent_launch(r->params[c], r->d_arrive[c], M, grid, r->stream);
         else
             for (int i = 0; i < n && lst == NVFP4_OK; ++i)
-                lst = launch_gemm(args_of(r->descs[i], M), r->stream, i > 0, ds);
+                lst = is_gemm(r->descs[i]) ? launch_gemm(args_of(r->descs[i], M), r->stream, i > 0, ds)
+                                           : launch_between(r->descs[i], r->between[i], M, r->stream);
         cudaGraph_t graph = nullptr;
         e = cudaStreamEndCapture(r->stream, &graph);
         r->graphs[M - 1] = graph;

@@ -11,6 +11,10 @@ attention output a_l for o, and the H just produced for down); no value
 flows from one layer to the next, so the numbers stay N(0,1)-scaled without
 norms while the graph is still one serial chain of nodes.
 
+With ``kv_heads`` the rounds are whole: the q/k/v output is rotated and appended
+to a paged cache of ``context`` committed slots per lane, the attention over it
+replaces the stand-in a_l, and o reads the attention's output.
+
 torch is used here for device memory only.
 """
 from __future__ import annotations
@@ -58,14 +62,21 @@ class SyntheticRound:
     vocab: int
     workload_id: int = 4
     gscale: float = synth.GSCALE
+    kv_heads: int = 0           # 0: stand-in attention output, no cache
+    head_dim: int = 128
+    context: int = 0            # committed slots per lane
+    page_size: int = 64
+    cache: object = None        # abi.Cache, every layer
     mats: dict = field(default_factory=dict)
     bufs: dict = field(default_factory=dict)
     descs: list = field(default_factory=list)
     nodes: list = field(default_factory=list)   # (name, kind, input key, output key, matrix keys)
 
     @classmethod
-    def build(cls, device, layers=64, hidden=5120, ffn=17408, vocab=151936, workload_id=4):
-        r = cls(torch.device(device), layers, hidden, ffn, vocab, workload_id)
+    def build(cls, device, layers=64, hidden=5120, ffn=17408, vocab=151936, workload_id=4, kv_heads=0, head_dim=128,
+              context=0, page_size=64):
+        r = cls(torch.device(device), layers, hidden, ffn, vocab, workload_id, kv_heads=kv_heads, head_dim=head_dim,
+                context=context, page_size=page_size)
         r._build()
         return r
 
@@ -75,16 +86,19 @@ class SyntheticRound:
     def _build(self):
         L, h, f, v, dev, wid = self.layers, self.hidden, self.ffn, self.vocab, self.device, self.workload_id
         M8 = abi_max_m()
+        qkv = 3 * h if not self.kv_heads else h + 2 * self.kv_heads * self.head_dim
+        if self.kv_heads:
+            self._build_cache()
         for l in range(L):
             base = 10 * l
-            self.mats[f"qkv{l}"] = make_matrix(wid, base + 0, 3 * h, h, dev)
+            self.mats[f"qkv{l}"] = make_matrix(wid, base + 0, qkv, h, dev)
             self.mats[f"o{l}"] = make_matrix(wid, base + 1, h, h, dev)
             self.mats[f"gate{l}"] = make_matrix(wid, base + 2, f, h, dev)
             self.mats[f"up{l}"] = make_matrix(wid, base + 3, f, h, dev)
             self.mats[f"down{l}"] = make_matrix(wid, base + 4, h, f, dev)
             self.bufs[f"x{l}"] = self._act(2 * l, h)
             self.bufs[f"a{l}"] = self._act(2 * l + 1, h)
-            self.bufs[f"yqkv{l}"] = torch.zeros((M8, 3 * h), dtype=torch.float32, device=dev)
+            self.bufs[f"yqkv{l}"] = torch.zeros((M8, qkv), dtype=torch.float32, device=dev)
             self.bufs[f"yo{l}"] = torch.zeros((M8, h), dtype=torch.float32, device=dev)
             self.bufs[f"H{l}"] = torch.zeros((M8, f), dtype=torch.bfloat16, device=dev)
             self.bufs[f"ydown{l}"] = torch.zeros((M8, h), dtype=torch.float32, device=dev)
@@ -94,10 +108,42 @@ class SyntheticRound:
         G, D = abi.NVFP4_DESC_GEMM, abi.NVFP4_DESC_GATEUP_SILU
         for l in range(L):
             self._node(f"qkv{l}", G, f"x{l}", f"yqkv{l}", [f"qkv{l}"])
+            if self.kv_heads:
+                self._attention_nodes(l)
             self._node(f"o{l}", G, f"a{l}", f"yo{l}", [f"o{l}"])
             self._node(f"gateup{l}", D, f"x{l}", f"H{l}", [f"gate{l}", f"up{l}"])
             self._node(f"down{l}", G, f"H{l}", f"ydown{l}", [f"down{l}"])
         self._node("head", G, "xhead", "logits", ["head"])
+
+    def _build_cache(self):
+        """A cache whose lanes hold `context` slots of drawn keys and values, with room for one more."""
+        lanes, page, dev = abi_max_m(), self.page_size, self.device
+        per = (self.context + 1 + page - 1) // page
+        self.cache = abi.Cache.empty(self.layers, lanes * per + lanes, self.kv_heads, page, self.head_dim, lanes,
+                                     per + 1, dev)
+        gen = torch.Generator(device=dev).manual_seed(self.workload_id)
+        self.cache.k.normal_(generator=gen)
+        self.cache.v.normal_(generator=gen)
+        self.bufs["want"] = torch.full((lanes,), self.context, dtype=torch.int32, device=dev)
+        self.cache.reserve(self.bufs["want"])
+        self.cache.compact(self.bufs["want"])
+        self.bufs["want"].fill_(1)
+        self.cache.reserve(self.bufs["want"])
+        half = self.head_dim // 2
+        self.bufs["inv_freq"] = 10000.0 ** (-torch.arange(half, dtype=torch.float64, device=dev) / half)
+        self.bufs["pos"] = torch.full((lanes,), self.context, dtype=torch.int32, device=dev)
+        heads = self.hidden // self.head_dim
+        self.bufs["q"] = torch.zeros((lanes, heads, self.head_dim), dtype=torch.bfloat16, device=dev)
+        self.bufs["attn_work"] = abi.attn_tree_workspace(self.cache, lanes, heads)
+
+    def _attention_nodes(self, l):
+        heads = self.hidden // self.head_dim
+        a = self.bufs[f"a{l}"]
+        self.descs.append(abi.desc_rope(self.cache, l, self.bufs[f"yqkv{l}"], heads, self.bufs["inv_freq"],
+                                        self.bufs["pos"], self.bufs["q"]))
+        self.nodes.append((f"rope{l}", abi.NVFP4_DESC_ROPE_APPEND, f"yqkv{l}", "q", []))
+        self.descs.append(abi.desc_attn(self.cache, l, self.bufs["q"], self.head_dim ** -0.5, a, self.bufs["attn_work"]))
+        self.nodes.append((f"attn{l}", abi.NVFP4_DESC_ATTN_TREE, "q", f"a{l}", []))
 
     def _node(self, name, kind, xin, out, mkeys):
         m0 = self.mats[mkeys[0]]
@@ -114,6 +160,14 @@ class SyntheticRound:
     def run_direct(self, M, stream=None):
         """The same chain as the graph, as direct C-ABI calls (no graph, no PDL)."""
         for (name, kind, xin, out, mkeys) in self.nodes:
+            if kind == abi.NVFP4_DESC_ROPE_APPEND:
+                abi.rope_append(self.cache, int(name[4:]), self.bufs[xin][:M], self.hidden // self.head_dim,
+                                self.bufs["inv_freq"], self.bufs["pos"][:M], q=self.bufs[out][:M], stream=stream)
+                continue
+            if kind == abi.NVFP4_DESC_ATTN_TREE:
+                abi.attn_tree(self.cache, int(name[4:]), self.bufs[xin][:M], self.head_dim ** -0.5,
+                              out=self.bufs[out][:M], workspace=self.bufs["attn_work"], stream=stream)
+                continue
             m0 = self.mats[mkeys[0]]
             X = self.bufs[xin][:M]
             if kind == abi.NVFP4_DESC_GEMM:

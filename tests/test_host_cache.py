@@ -115,6 +115,23 @@ def test_attention_workspace_sizes():
         assert st == abi.NVFP4_OK and 0 < n < 1 << 30
 
 
+def between(kind, args):
+    return abi.Nvfp4GemmDesc(kind, ctypes.cast(ctypes.pointer(args), ctypes.c_void_p))
+
+
+def test_round_refuses_nodes_it_cannot_run():
+    """One row per lane and 8 lanes, in a chained round; each node's own checks at 8 rows."""
+    ok8 = cache(lanes=8)
+    cases = [(between(2, rope(ok8, row_start=P, ldp=8)), 1, ARG), (between(3, attn(ok8, row_start=P)), 1, ARG),
+             (between(2, rope(cache(lanes=7), ldp=8)), 1, M), (between(3, attn(cache(lanes=4))), 1, M),
+             (between(2, rope(ok8, ldp=7)), 1, SHAPE), (between(3, attn(ok8, ldo=8)), 1, SHAPE),
+             (between(2, rope(cache(lanes=8, k=None), ldp=8)), 1, ARG), (between(2, rope(ok8, ldp=8)), 0, ARG),
+             (between(3, attn(ok8)), 0, ARG), (abi.Nvfp4GemmDesc(2, None), 1, ARG), (abi.Nvfp4GemmDesc(3, None), 1, ARG)]
+    for d, mode, status in cases:
+        st, h = abi.nvfp4_round_create_ex([d], mode)
+        assert (st, h) == (status, None)
+
+
 def beam(**kw):
     f = dict(logits=P, groups=2, beams=4, V=1000, ldv=1000, scores=P, finished=None, eos=2, scores_out=P, parent=P,
              token=P, finished_out=None, workspace=P, workspace_bytes=1 << 30, stream=None)
