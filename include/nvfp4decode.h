@@ -399,7 +399,7 @@ NVFP4_API int nvfp4_cache_fork(const nvfp4_cache* cache, const int32_t* parent, 
  * copy before its new pages.  want: device int32 [lanes], <= 0: nothing.
  * All or nothing: if the pool has too few free pages, or a lane would pass
  * max_pages, nothing changes, bit 256 of nvfp4_device_status() is set and *ok
- * is 0 (else 1).  ok: device int32, or NULL.  Two asynchronous launches.
+ * is 0 (else 1).  ok: device int32, or NULL.  One asynchronous launch.
  */
 NVFP4_API int nvfp4_cache_reserve(const nvfp4_cache* cache, const int32_t* want, int32_t* ok, nvfp4_stream_t stream);
 

@@ -59,39 +59,142 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const nvfp4_cache c,
 }
 
 // ------------------------------------------------------------- reserve
-// One CTA plans: how many pages each lane takes (a copy of its shared last
-// page, then the missing entries up to len + want), then the n-th page taken
-// is the n-th free one.  The copies go to scratch for the second kernel:
-// scratch[4 b ..] = {source page, destination page, filled slots, unused}.
-constexpr int kPlanThreads = 1024;
+// One launch plans, copies and applies.  Every CTA reads the same inputs and
+// comes to the same plan: how many pages each lane takes (a copy of its shared
+// last page, then the missing entries up to len + want); the n-th page taken is
+// the n-th free one.
+//   No copies: CTA 0 applies the plan.  A CTA that reads later, when tables have
+//   changed, still finds nothing to copy (no count of a last page changes).
+//   Copies: every CTA counts in when it has read all it needs, copies its share
+//   of the filled slots -- per (layer, k or v, head) one contiguous run -- and
+//   the last to count in applies the plan.
+constexpr int kResThreads = 512;
+constexpr int kResWarps = kResThreads / 32;
+constexpr int kResStep = 8 * kResThreads;  // page ids looked at in one step
 
-__global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const nvfp4_cache c, const int32_t* want,
-                                                                    int32_t* ok)
+struct Plan {
+    int need[kMaxLanes], first[kMaxLanes], copy[kMaxLanes], last[kMaxLanes], dst[kMaxLanes], fill[kMaxLanes],
+        col[kMaxLanes];
+    int start[kMaxLanes + 1];  // pages taken before lane b
+    int count[kResWarps];
+    int bad, copies, last_in;
+};
+
+// Walk the free pages in order of their ids, until `total` of them have gone
+// by: take(rank, page) for each.  Returns whether there are so many (all threads).
+template <class Take>
+__device__ bool walk_free(const nvfp4_cache& c, int total, Plan& s, Take take)
 {
-    __shared__ int s_need[kMaxLanes], s_first[kMaxLanes], s_copy[kMaxLanes], s_col[kMaxLanes], s_last[kMaxLanes];
-    __shared__ int s_start[kMaxLanes + 1];
-    __shared__ int s_bad, s_count[kPlanThreads / 32];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int given = 0;
+    for (int base = 0; base < c.pages && given < total; base += kResStep) {
+        // 8 neighbours a thread, loads in flight together
+        const int p0 = base + 8 * tid;
+        int n = 0;
+        unsigned free = 0;
+        int r[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) r[i] = p0 + i < c.pages ? c.ref[p0 + i] : 1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) free |= r[i] == 0 ? 1u << i : 0u;
+        n = __popc(free);
+        int incl = n;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
+        }
+        if (lane == 31) s.count[warp] = incl;
+        __syncthreads();  // every thread has read its ids' counts
+        int before = lane < kResWarps ? s.count[lane] : 0, all = before;
+#pragma unroll
+        for (int off = 1; off < kResWarps; off <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, all, off);
+            if (lane >= off) all += o;
+        }
+        before = __shfl_sync(0xffffffffu, all - before, warp);
+        all = __shfl_sync(0xffffffffu, all, kResWarps - 1);
+        int rank = given + before + incl - n;
+        for (; free && rank < total; free &= free - 1) take(rank++, p0 + __ffs(free) - 1);
+        given += all;
+        __syncthreads();
+    }
+    return given >= total;
+}
+
+// The filled slots of the copied pages, in every layer: 16-byte vectors, one
+// (lane, layer, k or v, head)'s run after the other, the grid's threads in line,
+// four loads of a thread in flight.  Bound by HBM: 37 MB read and written in
+// about 13 us at 64 layers (two or eight in flight measure the same).
+// I: an index type that holds a lane's vectors.
+template <class I>
+__device__ __forceinline__ void copy_slots(const nvfp4_cache& c, const Plan& s)
+{
+    const I runs = (I)c.layers * 2 * c.kv_heads, step = (I)gridDim.x * kResThreads;
+    const int64_t page = (int64_t)c.page_size * (c.head_dim / 8);  // vectors of a page and head
+    constexpr int kOnce = 4;
+    I i = (I)blockIdx.x * kResThreads + threadIdx.x;
+    int b = -1;
+    I n = 1, all = 0;
+    auto next_lane = [&] {  // i counts on from one lane's vectors to the next one's
+        i -= all;
+        do ++b; while (b < c.lanes && !s.copy[b]);
+        n = b < c.lanes ? s.fill[b] * (c.head_dim / 8) : 1;
+        all = b < c.lanes ? runs * n : 0;
+    };
+    next_lane();
+    while (b < c.lanes) {
+        uint4 x[kOnce];
+        uint4* to[kOnce];
+#pragma unroll
+        for (int z = 0; z < kOnce; ++z) {
+            while (b < c.lanes && i >= all) next_lane();
+            to[z] = nullptr;
+            if (b < c.lanes) {
+                const I r = i / n, q = r / c.kv_heads;
+                const int64_t at = (int64_t)(q / 2) * c.pages, h = (int64_t)(r - q * c.kv_heads), v = (int64_t)(i - r * n);
+                uint4* pool = (uint4*)(q & 1 ? c.v : c.k) + v + h * page;
+                x[z] = pool[(at + s.last[b]) * c.kv_heads * page];
+                to[z] = pool + (at + s.dst[b]) * c.kv_heads * page;
+                i += step;
+            }
+        }
+#pragma unroll
+        for (int z = 0; z < kOnce; ++z)
+            if (to[z]) *to[z] = x[z];
+    }
+}
+
+__global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache c, const int32_t* want, int32_t* ok)
+{
+    __shared__ Plan s;
     pdl_begin();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int shift = __ffs(c.page_size) - 1;
-    if (tid == 0) s_bad = 0;
+    if (tid == 0) {
+        s.bad = 0;
+        s.copies = 0;
+    }
     if (tid < kMaxLanes) {
-        s_need[tid] = 0;
-        s_copy[tid] = 0;
-        s_last[tid] = -1;
+        s.need[tid] = 0;
+        s.copy[tid] = 0;
+        s.last[tid] = -1;
+        s.dst[tid] = -1;
     }
     __syncthreads();
-    // a warp per lane: the missing entries
-    for (int b = warp; b < c.lanes; b += kPlanThreads / 32) {
+    // a warp per lane: the missing entries, and the count of a partly filled last page
+    for (int b = warp; b < c.lanes; b += kResWarps) {
         const int w = want[b], n = max(c.len[b], 0);
         if (w <= 0) continue;
         const int32_t* row = c.table + (int64_t)b * c.max_pages;
         const int64_t end = (int64_t)n + w;
         if (end > (int64_t)c.max_pages << shift) {
-            if (lane == 0) s_bad = 1;
+            if (lane == 0) s.bad = 1;
             continue;
         }
         const int c0 = (n + c.page_size - 1) >> shift, c1 = (int)((end + c.page_size - 1) >> shift);
+        const bool partly = n & (c.page_size - 1);
+        const int p = partly ? row[n >> shift] : -1;
         int first = c1;  // entries from here on are -1: a lane's pages come first
         for (int q = c0; q < c1; q += 32) {
             const int e = q + lane < c1 ? row[q + lane] : 0;
@@ -102,149 +205,86 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_plan_kernel(const nvfp4_
             }
         }
         if (lane == 0) {
-            s_need[b] = c1 - first;
-            s_first[b] = first;
-            if (n & (c.page_size - 1)) {
-                const int p = row[n >> shift];
-                s_col[b] = n >> shift;
-                if (p >= 0 && p < c.pages)
-                    s_last[b] = p;
-                else
+            s.need[b] = c1 - first;
+            s.first[b] = first;
+            s.fill[b] = n & (c.page_size - 1);
+            s.col[b] = n >> shift;
+            if (partly) {
+                if (p >= 0 && p < c.pages) {
+                    s.last[b] = p;
+                    s.copy[b] = c.ref[p];
+                } else if (blockIdx.x == 0) {
                     atomicOr(&g_cache_status, kRefused);
+                }
             }
         }
     }
     __syncthreads();
     // which lanes copy their last page: in lane order, all but the last holder
-    if (tid < c.lanes && s_last[tid] >= 0) {
+    int mine = 0;
+    if (tid < kMaxLanes && s.last[tid] >= 0) {
         int before = 0;
-        for (int b = 0; b < tid; ++b) before += s_last[b] == s_last[tid];
-        s_copy[tid] = c.ref[s_last[tid]] - before > 1;
+        for (int b = 0; b < tid; ++b) before += s.last[b] == s.last[tid];
+        mine = s.copy[tid] - before > 1;
     }
     __syncthreads();
-    if (tid == 0) {
-        int64_t sum = 0;
-        for (int b = 0; b < c.lanes; ++b) {
-            s_start[b] = (int)sum;
-            sum += s_need[b] + s_copy[b];
-            if (sum > c.pages) sum = (int64_t)c.pages + 1;  // more than there are: refused below
-        }
-        s_start[c.lanes] = (int)sum;
+    if (tid < kMaxLanes) {
+        s.copy[tid] = mine;
+        if (mine) s.copies = 1;
     }
     __syncthreads();
-    const int total = s_start[c.lanes];
-    // Free pages in order of their ids, 4 ids per thread and step: count until
-    // there are enough, then hand them out.
-    bool enough = total == 0 && !s_bad;
-    if (!enough && !s_bad) {
-        int seen = 0;
-        for (int base = 0; base < c.pages && seen < total; base += 4 * kPlanThreads) {
-            int n = 0;
+    if (warp == 0) {
+        // sums over the lanes, two a thread, held at one more than there are pages
+        const long long x0 = s.need[2 * lane] + s.copy[2 * lane], x1 = s.need[2 * lane + 1] + s.copy[2 * lane + 1];
+        long long incl = x0 + x1;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int p = base + 4 * tid + i;
-                n += p < c.pages && c.ref[p] == 0;
-            }
-            n = __reduce_add_sync(0xffffffffu, n);
-            if (lane == 0) s_count[warp] = n;
-            __syncthreads();
-            for (int i = 0; i < kPlanThreads / 32; ++i) seen += s_count[i];
-            __syncthreads();
+        for (int off = 1; off < 32; off <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, incl, off);
+            if (lane >= off) incl += o;
         }
-        enough = seen >= total;
+        const long long most = (long long)c.pages + 1;
+        s.start[2 * lane] = (int)min(incl - x0 - x1, most);
+        s.start[2 * lane + 1] = (int)min(incl - x1, most);
+        if (lane == 31) s.start[kMaxLanes] = (int)min(incl, most);
     }
-    if (tid < c.lanes) {
-        c.scratch[4 * tid] = enough && s_copy[tid] ? s_last[tid] : -1;
-        c.scratch[4 * tid + 2] = max(c.len[tid], 0) & (c.page_size - 1);
+    __syncthreads();
+    const int total = s.start[kMaxLanes];
+    bool enough = !s.bad && total <= c.pages, apply = blockIdx.x == 0;
+    unsigned* counter = (unsigned*)c.scratch + 4 * c.lanes;
+    if (s.copies) {
+        if (enough)
+            enough = walk_free(c, total, s, [&](int rank, int page) {
+                int b = 0;
+                while (s.start[b + 1] <= rank) ++b;
+                if (s.copy[b] && rank == s.start[b]) s.dst[b] = page;
+            });
+        __syncthreads();
+        if (tid == 0) s.last_in = count_in(counter) == gridDim.x - 1;
+        __syncthreads();
+        apply = s.last_in;
+        if (enough) {
+            if ((int64_t)c.layers * 2 * c.kv_heads * c.page_size * c.head_dim / 8 < (int64_t)1 << 31)
+                copy_slots<uint32_t>(c, s);
+            else
+                copy_slots<uint64_t>(c, s);
+        }
     }
+    if (!apply) return;
+    if (enough)
+        enough = walk_free(c, total, s, [](int, int) {});
+    if (enough)
+        walk_free(c, total, s, [&](int rank, int page) {
+            int b = 0;
+            while (s.start[b + 1] <= rank) ++b;
+            const int nth = rank - s.start[b] - s.copy[b];
+            c.table[(int64_t)b * c.max_pages + (nth < 0 ? s.col[b] : s.first[b] + nth)] = page;
+            c.ref[page] = 1;
+        });
+    if (enough && tid < c.lanes && s.copy[tid]) atomicSub(c.ref + s.last[tid], 1);
     if (tid == 0) {
         if (ok) *ok = enough ? 1 : 0;
         if (!enough) atomicOr(&g_cache_status, kNoPages);
-    }
-    if (!enough || total == 0) return;
-    __syncthreads();
-    int given = 0;
-    for (int base = 0; given < total; base += 4 * kPlanThreads) {
-        int n = 0;
-        unsigned freem = 0;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int p = base + 4 * tid + i;
-            if (p < c.pages && c.ref[p] == 0) {
-                freem |= 1u << i;
-                ++n;
-            }
-        }
-        int incl = n;
-#pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int o = __shfl_up_sync(0xffffffffu, incl, off);
-            if (lane >= off) incl += o;
-        }
-        if (lane == 31) s_count[warp] = incl;
-        __syncthreads();  // every thread has read its ids' counts
-        int rank = given + incl - n, all = 0;
-        for (int i = 0; i < kPlanThreads / 32; ++i) {
-            if (i < warp) rank += s_count[i];
-            all += s_count[i];
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (!((freem >> i) & 1)) continue;
-            if (rank < total) {
-                int b = 0;
-                while (s_start[b + 1] <= rank) ++b;
-                int nth = rank - s_start[b];
-                const int p = base + 4 * tid + i;
-                int col;
-                if (s_copy[b] && nth == 0) {
-                    col = s_col[b];
-                    c.scratch[4 * b + 1] = p;
-                } else {
-                    col = s_first[b] + nth - s_copy[b];
-                }
-                c.table[(int64_t)b * c.max_pages + col] = p;
-                c.ref[p] = 1;
-            }
-            ++rank;
-        }
-        given += all;
-        __syncthreads();
-    }
-    if (tid < c.lanes && s_copy[tid]) atomicSub(c.ref + s_last[tid], 1);
-}
-
-// The planned copies: the filled slots of a page, per (layer, k or v, head) one
-// contiguous run, spread over the grid.
-constexpr int kCopyThreads = 256;
-
-__global__ void __launch_bounds__(kCopyThreads) page_copy_kernel(const nvfp4_cache c)
-{
-    __shared__ int lanes_of[kMaxLanes];
-    __shared__ int s_n;
-    pdl_begin();
-    const int tid = threadIdx.x;
-    if (tid == 0) {
-        int n = 0;
-        for (int b = 0; b < c.lanes; ++b)
-            if (c.scratch[4 * b] >= 0) lanes_of[n++] = b;
-        s_n = n;
-    }
-    __syncthreads();
-    const int64_t per = (int64_t)c.layers * 2 * c.kv_heads;
-    const int64_t segs = per * s_n;
-    for (int64_t s = blockIdx.x; s < segs; s += gridDim.x) {
-        const int b = lanes_of[s / per];
-        const int64_t r = s % per;
-        const int h = (int)(r % c.kv_heads), kv = (int)(r / c.kv_heads & 1);
-        const int64_t layer = r / c.kv_heads / 2;
-        const int64_t run = (int64_t)c.page_size * c.head_dim;  // elements of a page and head
-        uint16_t* pool = (uint16_t*)(kv ? c.v : c.k);
-        const int64_t at = layer * c.pages;
-        const uint4* src = (const uint4*)(pool + ((at + c.scratch[4 * b]) * c.kv_heads + h) * run);
-        uint4* dst = (uint4*)(pool + ((at + c.scratch[4 * b + 1]) * c.kv_heads + h) * run);
-        const int n = c.scratch[4 * b + 2] * (c.head_dim / 8);
-        for (int i = tid; i < n; i += kCopyThreads) dst[i] = src[i];
+        if (s.copies) *counter = 0u;
     }
 }
 
@@ -280,7 +320,7 @@ __global__ void __launch_bounds__(256) trim_kernel(const nvfp4_cache c, const in
 // (lane, layer, k or v, head) and moves its slots in ascending order, up to 8
 // at a time: sources ascend strictly and none lies before its target, so a
 // later source is never an earlier target of another batch.  The last CTA to
-// finish commits lengths and releases pages.
+// have read its lane commits lengths and releases pages.
 constexpr int kMoveThreads = 256;
 
 struct MoveLane {
@@ -290,6 +330,7 @@ struct MoveLane {
     int32_t to_row[NVFP4_ATTN_MAX_ROWS];
     int count;  // slots to look at, from `first` on; 0: none moves
     int first;  // the slots before it lie where they belong
+    int len;    // before the commit
     int good;
 };
 
@@ -299,17 +340,18 @@ __device__ void read_lane(const nvfp4_cache& c, int b, const int32_t* count, con
 {
     const int shift = __ffs(c.page_size) - 1;
     const int n = max(c.len[b], 0), k = count[b];
+    const int s = path && tid < ld ? path[(int64_t)b * ld + tid] : 0;
+    const int before = path && tid && tid < ld ? path[(int64_t)b * ld + tid - 1] : -1;
+    const int32_t* row = c.table + (int64_t)b * c.max_pages;
+    const int64_t cap = (int64_t)c.max_pages << shift;
+    bool fine = k >= 0 && (!path || k <= ld) && (int64_t)n + k <= cap;
     if (tid == 0) {
-        m.good = k >= 0 && (!path || k <= ld) && (int64_t)n + k <= (int64_t)c.max_pages << shift;
-        m.count = 0;
         m.first = NVFP4_ATTN_MAX_ROWS;
+        m.len = n;
     }
     __syncthreads();
-    if (path && m.good && tid < k) {
-        const int32_t* row = c.table + (int64_t)b * c.max_pages;
-        const int s = path[(int64_t)b * ld + tid];
-        const int before = tid ? path[(int64_t)b * ld + tid - 1] : -1;
-        bool fine = s > before && s < NVFP4_ATTN_MAX_ROWS && (int64_t)n + s < (int64_t)c.max_pages << shift;
+    if (path && fine && tid < k) {
+        fine = s > before && s < NVFP4_ATTN_MAX_ROWS && (int64_t)n + s < cap;
         if (fine) {
             const int from = n + s, to = n + tid;
             const int fp = row[from >> shift], tp = row[to >> shift];
@@ -320,18 +362,13 @@ __device__ void read_lane(const nvfp4_cache& c, int b, const int32_t* count, con
             m.to_row[tid] = to & (c.page_size - 1);
             if (s != tid) atomicMin(&m.first, tid);
         }
-        if (!fine) atomicAnd(&m.good, 0);
-    } else if (!path && m.good && k > 0) {
+    } else if (!path && fine && k > 0) {
         // kept as they lie: the slots need pages
-        const int32_t* row = c.table + (int64_t)b * c.max_pages;
-        bool fine = true;
         for (int q = (n >> shift) + tid; q <= (n + k - 1) >> shift; q += blockDim.x)
             fine = fine && row[q] >= 0 && row[q] < c.pages;
-        if (!fine) atomicAnd(&m.good, 0);
     }
-    __syncthreads();
-    if (tid == 0 && path && m.good) m.count = k;
-    __syncthreads();
+    m.count = path ? k : 0;  // the same in every thread
+    m.good = __syncthreads_and(fine);
 }
 
 template <int D>
@@ -345,6 +382,13 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const nvfp4_cache
     const int tid = threadIdx.x;
     const int b = blockIdx.y;
     read_lane(c, b, count, path, ld, tid, m);
+    // What the commit changes has been read: count in before the moves, which go
+    // on while the last CTA commits.  Each lane's new length, or -1, is in scratch.
+    unsigned* counter = (unsigned*)c.scratch + 4 * c.lanes;
+    if (tid == 0) {
+        if (blockIdx.x == 0) c.scratch[b] = m.good ? m.len + count[b] : -1;
+        s_last = count_in(counter) == gridDim.x * gridDim.y - 1;
+    }
     if (path && m.good) {
         const int64_t segs = (int64_t)c.layers * 2 * c.kv_heads;
         const int64_t run = (int64_t)c.page_size * D;
@@ -364,23 +408,15 @@ __global__ void __launch_bounds__(kMoveThreads) compact_kernel(const nvfp4_cache
             }
         }
     }
-    // The last CTA commits, a warp per lane: every CTA has read lengths, paths
-    // and tables by then, and left its lane's verdict in scratch.
-    unsigned* counter = (unsigned*)c.scratch + 4 * c.lanes;
-    if (tid == 0) {
-        if (blockIdx.x == 0) c.scratch[4 * b + 3] = m.good;
-        s_last = count_in(counter) == gridDim.x * gridDim.y - 1;
-    }
     __syncthreads();
     if (!s_last) return;
     const int lane = tid & 31;
     for (int l = tid >> 5; l < c.lanes; l += kMoveThreads / 32) {
-        if (!__ldcg(c.scratch + 4 * l + 3)) {
+        const int n = __ldcg(c.scratch + l);
+        if (n < 0) {
             if (lane == 0) atomicOr(&g_cache_status, kRefused);
             continue;
         }
-        const int n = max(c.len[l], 0) + count[l];
-        __syncwarp();
         if (lane == 0) c.len[l] = n;
         int32_t* row = c.table + (int64_t)l * c.max_pages;
         bool more = true;  // a lane's pages come first: the scan ends with the first stretch without one
@@ -437,8 +473,7 @@ extern "C" int nvfp4_cache_reserve(const nvfp4_cache* cache, const int32_t* want
     int sms = 0;
     st = sm_count(&sms);
     if (st != NVFP4_OK) return st;
-    NVFP4_CUDA_TRY(launch_pdl(reserve_plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, *cache, want, ok));
-    NVFP4_CUDA_TRY(launch_pdl(page_copy_kernel, dim3((unsigned)(8 * sms)), dim3(kCopyThreads), 0, stream, *cache));
+    NVFP4_CUDA_TRY(launch_pdl(reserve_kernel, dim3((unsigned)(2 * sms)), dim3(kResThreads), 0, stream, *cache, want, ok));
     return NVFP4_OK;
 }
 
