@@ -490,8 +490,8 @@ NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stre
  * FP32; the weights exp(s - max) are rounded to bf16 for the product with v.
  *
  * Limits: 1 <= rows <= NVFP4_ATTN_MAX_ROWS, the verify width (NVFP4_ERR_M);
- * q_heads a multiple of kv_heads and at most 32 times it, 0 <= layer < layers
- * (NVFP4_ERR_SHAPE).  max_nodes: the most rows a lane is expected to have, at
+ * q_heads a multiple of kv_heads and at most 32 times it, 0 <= layer < layers,
+ * lanes * kv_heads * (max_pages * page_size / 128 + 5) < 2^30 (NVFP4_ERR_SHAPE).  max_nodes: the most rows a lane is expected to have, at
  * least 1; it only chooses the tiling.  Results are the same from call to call.
  *
  * workspace: device, 16-byte aligned, of nvfp4_attn_tree_workspace() bytes

@@ -342,10 +342,18 @@ struct Segment {
     int next;         // the unit after the segment
 };
 
-__device__ __forceinline__ int range_begin(int units, int groups, int g) { return (int)((int64_t)units * g / groups); }
+// (In 32 bits where the product fits: a 64-bit division takes some 500 cycles,
+// and the first page is fetched only after it.)
+constexpr int kSmallUnits = 1 << 23;  // times at most 512 groups
+__device__ __forceinline__ int range_begin(int units, int groups, int g)
+{
+    return units < kSmallUnits ? (int)((uint32_t)units * (uint32_t)g / (uint32_t)groups)
+                               : (int)((int64_t)units * g / groups);
+}
 __device__ __forceinline__ int range_owner(int units, int groups, int u)
 {
-    return (int)((((int64_t)u + 1) * groups - 1) / units);
+    return units < kSmallUnits ? (int)((((uint32_t)u + 1) * (uint32_t)groups - 1) / (uint32_t)units)
+                               : (int)((((int64_t)u + 1) * groups - 1) / units);
 }
 
 // The lanes' rows, lengths and tiles, and the groups, for a whole CTA (two
@@ -1172,6 +1180,7 @@ int validate_attn(const nvfp4_attn_args* a)
     const int64_t width = (int64_t)a->q_heads * c->head_dim;
     if (a->layer < 0 || a->layer >= c->layers || a->q_heads < 1 || a->q_heads % c->kv_heads ||
         a->q_heads > 32 * c->kv_heads || a->max_nodes < 1 || a->ldq < width || a->ldo < width ||
+        (int64_t)c->lanes * c->kv_heads * ((int64_t)c->max_pages * c->page_size / kTile + 1 + kStart) >= (1 << 30) ||
         a->ldq > ((int64_t)1 << 38) || a->ldo > ((int64_t)1 << 40))
         return NVFP4_ERR_SHAPE;
     if (!aligned16(a->q) || !aligned16(a->out) || !aligned16(a->workspace) || (a->ldq & 7) || (a->ldo & 7) ||
@@ -1209,6 +1218,7 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     st = query_map(encode, *a, g, p.q_box, &mq);
     if (st != NVFP4_OK) return st;
     if (sms < NVFP4_ATTN_MAX_ROWS) return fail_cuda(cudaErrorInvalidDevice);
+    if (p.ctas > 512) p.ctas = 512;  // what the schedule's arithmetic takes
     return p.c.head_dim == 64    ? launch_dim<64>(n, p, mk, mv, mq, stream)
            : p.c.head_dim == 128 ? launch_dim<128>(n, p, mk, mv, mq, stream)
                                  : launch_dim<256>(n, p, mk, mv, mq, stream);

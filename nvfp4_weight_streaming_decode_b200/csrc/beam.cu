@@ -4,8 +4,9 @@
 //
 // Within a row candidates rank as their logits do, so no row needs more than
 // its `beams` largest logits, and its normaliser: row m is cut into S slices,
-// one CTA each, which keeps its slice in registers, takes its maximum, the sum
-// of exp(x - max) and its `beams` best (value, index).  The last CTA of a group
+// one CTA each, which reads its slice once for the maximum and the sum of
+// exp(x - max) -- running, a thread at a time -- and then again, from L2 and only
+// the threads that have one, for its `beams` best (value, index).  The last CTA of a group
 // to finish (counter, acquire/release) joins the normalisers in slice order and
 // ranks the group's beams * S * beams candidates by 64-bit scores.
 //
@@ -26,16 +27,14 @@ namespace nvfp4 {
 
 namespace {
 
-// 256 threads of 32 logits: steps that do not grow with the slice (bounds, sums
-// across lanes, ranking) are issue-bound, so not fewer logits a thread; and the
-// code for a thread's logits runs once, so it is kept short (hits as a bit mask,
-// their values fetched again) -- fetching instructions would cost more.
 constexpr int kBeamThreads = 256;
-constexpr int kPerThread = 32;                          // logits a thread holds
-constexpr int kSliceMax = kBeamThreads * kPerThread;    // 8192
-static_assert(kPerThread <= 32, "a bit of a word per logit");
+constexpr int kChunk = 16;                              // logits a thread takes at a time
+constexpr int kStride = 4 * kBeamThreads;               // columns of one round of float4
+constexpr int kParts = 16;                              // of a thread's columns, for the second reading
+constexpr int kCtasPerSm = 3;
 constexpr int kWarps = kBeamThreads / 32;
 constexpr int kListCap = 512;
+constexpr int kHeld = 8;                                // candidates a merging thread holds
 constexpr int kMaxRows = NVFP4_TOPK_MAX_ROWS;
 
 struct alignas(16) SlicePart {
@@ -60,13 +59,24 @@ struct BeamParams {
     unsigned* counters; // [groups]
 };
 
-// e^x by the exponential unit, within about 2^-22 (1 + |x| / 8) of itself; terms
-// far below the maximum, where that grows, hardly count in the sum.
-__device__ __forceinline__ float exp_fast(float x)
+// 2^x by the exponential unit, within about 2^-22 of itself.  With x = (logit -
+// maximum) log2(e) rounded, a term is off by 2^-24 (1 + |x|) more: those far
+// below the maximum, where that grows, hardly count in the sum.
+__device__ __forceinline__ float exp2_fast(float x)
 {
     float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+// (a - ref) log2(e) and (b - ref) log2(e), as pairs.
+__device__ __forceinline__ float2 scaled(float a, float b, float ref)
+{
+    float2 r;
+    asm("{\n .reg .b64 v, m, l;\n mov.b64 v, {%2, %3};\n mov.b64 m, {%4, %4};\n mov.b64 l, {%5, %5};\n"
+        " add.rn.f32x2 v, v, m;\n mul.rn.f32x2 v, v, l;\n mov.b64 {%0, %1}, v;\n}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a), "f"(b), "f"(-ref), "f"(1.4426950408889634f));
+    return r;
 }
 
 // An order on (value, place): the larger value first, equal ones by lower place.
@@ -87,14 +97,31 @@ struct ListShared {
     int count;
 };
 
+// The value as bits that order as it does.
+__device__ __forceinline__ uint32_t order_bits(float v)
+{
+    const uint32_t b = __float_as_uint(v);
+    return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+
 // A warp's bound: the k-th largest (k <= 32) of its lanes' values goes to *out.
-template <class T>
-__device__ __forceinline__ void warp_kth(int k, T mine, int lane, T* out)
+__device__ __forceinline__ void warp_kth(int k, float mine, int lane, float* out)
+{
+    // k - 1 times the largest leaves (one lane of it); the largest of the rest
+    uint32_t key = order_bits(mine);
+    for (int i = 1; i < k; ++i) {
+        const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+        if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) key = 0u;
+    }
+    const uint32_t top = __reduce_max_sync(0xffffffffu, key);
+    if (lane == __ffs(__ballot_sync(0xffffffffu, key == top)) - 1) *out = mine;
+}
+__device__ __forceinline__ void warp_kth(int k, double mine, int lane, double* out)
 {
     int rank = 0;
 #pragma unroll
     for (int i = 0; i < 32; ++i) {
-        const T o = __shfl_sync(0xffffffffu, mine, i);
+        const double o = __shfl_sync(0xffffffffu, mine, i);
         rank += o > mine || (o == mine && i < lane);
     }
     if (rank == k - 1) *out = mine;
@@ -205,6 +232,7 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
         ListShared<float> f;
         ListShared<double> d;
     } sh;
+    __shared__ float s_part[kParts][kBeamThreads];
     __shared__ float s_w[kWarps];
     __shared__ double s_d[kWarps];
     __shared__ double s_lse[kMaxRows], s_cum[kMaxRows];
@@ -217,41 +245,60 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     const bool done = p.finished && p.finished[m] != 0;
     const long long at = (long long)m * p.S + s;
     if (!done) {
-        // 1. the slice, thread t holding columns lo + 4 t + 1024 i + (0..3)
+        // 1. The thread's running maximum and sum of exp(x - maximum) over its
+        // columns lo + 4 tid + 1024 i + (0..3): once through memory, a chunk of
+        // loads in flight at a time.
         const int lo = s * p.slice, n = min(p.slice, p.V - lo);
         const float* x = p.logits + (long long)m * p.ldv + lo;
-        float r[kPerThread];
-#pragma unroll
-        for (int i = 0; i < kPerThread / 4; ++i) {
-            const int q = 4 * tid + 4 * kBeamThreads * i;
+        auto four = [&](int q) {  // columns q .. q + 3 of the slice, -inf behind it
             float4 v = make_float4(kNone, kNone, kNone, kNone);
             if (q + 4 <= n) {
-                v = __ldcs(reinterpret_cast<const float4*>(x + q));
+                v = __ldg(reinterpret_cast<const float4*>(x + q));
             } else if (q < n) {
                 v.x = x[q];
                 if (q + 1 < n) v.y = x[q + 1];
                 if (q + 2 < n) v.z = x[q + 2];
             }
-            r[4 * i] = v.x;
-            r[4 * i + 1] = v.y;
-            r[4 * i + 2] = v.z;
-            r[4 * i + 3] = v.w;
-        }
-        // 2. each warp's maximum, its sum of exp(x - maximum) (32 bits
-        // within a thread, 64 bits from there on: the joined normaliser is then
-        // good to about 1e-7 and mostly far better, which keeps near ties of
-        // different beams in their order) and its bound for the selection
-        float mine = kNone;
+            return v;
+        };
+        // The maxima of up to kParts parts of the columns stay in shared memory: the
+        // selection reads only parts that hold something for it again.
+        const int rounds = (n + kChunk / 4 * kStride - 1) / (kChunk / 4 * kStride), per_part = (rounds + kParts - 1) / kParts;
+        float mine = kNone, acc = 0.f, part_top = kNone;
+        for (int c = 0; c < rounds; ++c) {
+            const int q0 = 4 * tid + c * (kChunk / 4 * kStride);
+            float4 v[kChunk / 4];
 #pragma unroll
-        for (int i = 0; i < kPerThread; ++i) mine = fmaxf(mine, r[i]);
+            for (int i = 0; i < kChunk / 4; ++i) v[i] = four(q0 + i * kStride);
+            float here = kNone;
+#pragma unroll
+            for (int i = 0; i < kChunk / 4; ++i)
+                here = fmaxf(fmaxf(fmaxf(here, v[i].x), fmaxf(v[i].y, v[i].z)), v[i].w);
+            part_top = fmaxf(part_top, here);
+            if ((c + 1) % per_part == 0 || c + 1 == rounds) {
+                s_part[c / per_part][tid] = part_top;
+                part_top = kNone;
+            }
+            const float top = fmaxf(mine, here);
+            const float ref = top == kNone ? 0.f : top;  // nothing but -inf so far (or NaN, which the sum keeps)
+            float e0 = 0.f, e1 = 0.f;
+#pragma unroll
+            for (int i = 0; i < kChunk / 4; ++i) {
+                // (x - maximum) log2(e), two at a time
+                const float2 a = scaled(v[i].x, v[i].y, ref), b = scaled(v[i].z, v[i].w, ref);
+                e0 += exp2_fast(a.x) + exp2_fast(a.y);
+                e1 += exp2_fast(b.x) + exp2_fast(b.y);
+            }
+            acc = acc * (mine == top ? 1.f : expf(mine - top)) + (e0 + e1);
+            mine = top;
+        }
+        // 2. the warps' maxima, sums and bounds for the selection; 64 bits from here
+        // on (the joined normaliser is good to about 1e-7 and mostly far better,
+        // which keeps near ties of different beams in their order)
         float top = mine;
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-        const float ref = top == kNone ? 0.f : top;  // nothing but -inf (or NaN, which the sum keeps)
-        float e[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int i = 0; i < kPerThread; ++i) e[i % 4] += exp_fast(r[i] - ref);
-        double sum = (double)((e[0] + e[1]) + (e[2] + e[3]));
+        double sum = (double)acc * (double)(mine == top ? 1.f : expf(mine - top));
 #pragma unroll
         for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
         if (lane == 0) {
@@ -282,17 +329,35 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
             p.beams, mine, kNone,
             [&](float bound, auto f) {
                 bound = fmaxf(bound, -FLT_MAX);  // never -inf
-                uint32_t hits = 0;
+                // this thread has one: through its parts that do again (L2 holds them)
+                // -- each lane its own next one, so that a warp waits for memory about once
+                uint32_t todo = 0;
+                for (int c = 0; c * per_part < rounds; ++c) todo |= s_part[c][tid] >= bound ? 1u << c : 0u;
+                for (int c = 0, end = 0; todo || c < end; ++c) {
+                    if (c >= end) {
+                        const int part = __ffs(todo) - 1;
+                        todo &= todo - 1;
+                        c = part * per_part;
+                        end = min(c + per_part, rounds);
+                    }
+                    const int q0 = 4 * tid + c * (kChunk / 4 * kStride);
+                    float4 v[kChunk / 4];
 #pragma unroll
-                for (int i = 0; i < kPerThread; ++i) hits |= r[i] >= bound ? 1u << i : 0u;
-                for (; hits; hits &= hits - 1) {
-                    const int i = __ffs(hits) - 1, q = 4 * tid + 4 * kBeamThreads * (i / 4) + i % 4;
-                    f(__ldg(x + q), (uint32_t)(lo + q));
+                    for (int i = 0; i < kChunk / 4; ++i) v[i] = four(q0 + i * kStride);
+                    uint32_t hits = 0;
+#pragma unroll
+                    for (int i = 0; i < kChunk / 4; ++i)
+                        hits |= (v[i].x >= bound ? 1u << 4 * i : 0u) | (v[i].y >= bound ? 2u << 4 * i : 0u) |
+                                (v[i].z >= bound ? 4u << 4 * i : 0u) | (v[i].w >= bound ? 8u << 4 * i : 0u);
+                    for (; hits; hits &= hits - 1) {  // (each lane its own next hit, for the same reason)
+                        const int i = __ffs(hits) - 1, q = q0 + (i >> 2) * kStride + (i & 3);
+                        f(__ldg(x + q), (uint32_t)(lo + q));
+                    }
                 }
             },
             [&](auto f) {
                 for (int q = tid; q < n; q += kBeamThreads) {
-                    const float v = __ldg(x + q);
+                    const float v = x[q];
                     if (v > kNone) f(v, (uint32_t)(lo + q));
                 }
             },
@@ -311,7 +376,6 @@ __global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams 
     // Candidate i of the group is place q = i % per of row w = i / per.  Up to
     // kHeld per thread are fetched at once, before the normalisers they need.
     const int per = p.S * p.beams, n = p.beams * per;
-    constexpr int kHeld = 8;
     const bool held = n <= kHeld * kBeamThreads;
     float hx[kHeld];
     int hv[kHeld];
@@ -438,13 +502,15 @@ int beam_split(int groups, int beams, int64_t V, int sms, BeamSplit* b)
         return NVFP4_ERR_M;
     if (V < 1 || V > (1 << 20)) return NVFP4_ERR_SHAPE;
     const int rows = groups * beams;
-    // Slices of at most kSliceMax, otherwise two CTAs per SM over all rows, at
-    // least 1024 logits each.
-    int64_t S = (V + kSliceMax - 1) / kSliceMax;
-    int64_t want = (2LL * sms + rows - 1) / rows;
-    const int64_t most = (V + 1023) / 1024;
-    if (want > most) want = most;
-    if (S < want) S = want;
+    // One turn of the GPU at three CTAs an SM (two to four measure the same), slices of at least 2048 logits, and
+    // where it costs no more than three quarters of the CTAs, few enough
+    // candidates for the merge to hold in registers (beyond, it fetches them
+    // three times).
+    int64_t S = (int64_t)kCtasPerSm * sms / rows;
+    const int64_t most = (V + 2047) / 2048, held = kHeld * kBeamThreads / (beams * beams);
+    if (S > most) S = most;
+    if (S > held) S = held > (S + 3) / 4 ? held : (S + 3) / 4;
+    if (S < 1) S = 1;
     int64_t slice = (V + S - 1) / S;
     slice = (slice + 3) / 4 * 4;
     b->S = (int)((V + slice - 1) / slice);

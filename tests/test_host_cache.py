@@ -104,6 +104,12 @@ def test_attention_refuses(kw, status):
     assert abi.nvfp4_attn_tree(ctypes.byref(attn(**kw)), None) == status
 
 
+def test_attention_refuses_tables_past_its_schedule():
+    c = cache(lanes=64, kv_heads=256, pages=1024, page_size=256, max_pages=1 << 17)
+    a = attn(c, q_heads=256, ldq=256 * 128, ldo=256 * 128)
+    assert abi.nvfp4_attn_tree(ctypes.byref(a), None) == SHAPE
+
+
 def test_attention_workspace_sizes():
     assert abi.nvfp4_attn_tree_workspace(8, 40, 8, 128, 0)[0] == ARG
     assert abi.nvfp4_attn_tree_workspace(0, 40, 8, 128, 148)[0] == M
