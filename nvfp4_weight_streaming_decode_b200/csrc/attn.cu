@@ -12,8 +12,8 @@
 // columns instead of a padded tile of rows: one row and eight drafts run the
 // same code at the same memory rate.
 //
-// The reference m of a column is the maximum of the first tile that shows it a
-// slot, not the running maximum: weights up to 2^kHeadroom are as exact in
+// The reference m of a column is the maximum of a segment's first tile (or the
+// first to show it a slot), not the running maximum: weights up to 2^kHeadroom are as exact in
 // FP32 and bf16 as weights below 1 (both hold powers of two that far), so
 // O^T is rescaled only when a score passes m by more than that -- rarely, by a
 // vote of the 128 threads that share the columns.
@@ -470,7 +470,55 @@ __device__ __forceinline__ float weigh(float (&x)[C], uint8_t* prow)
     return over;
 }
 
-// ------------------------------------------------------------ new references
+// ------------------------------------------------------------ references
+
+// The maxima over a warp's 32 slots of C columns, to out[column].  Halving: each
+// step a lane keeps half of its columns and takes the other lane's maxima of
+// them, C - 1 exchanges in all where one column after the other would take 5 C.
+template <int C>
+__device__ __forceinline__ void column_max(const float (&x)[C], int lane, float* out)
+{
+    constexpr int W = C < 32 ? C : 32;
+#pragma unroll
+    for (int g = 0; g < C; g += W) {
+        float y[W / 2];
+#pragma unroll
+        for (int w = W / 2; w > 0; w >>= 1) {
+            const bool upper = lane & w;
+#pragma unroll
+            for (int i = 0; i < w; ++i) {
+                const float a = w == W / 2 ? x[g + i] : y[i], b = w == W / 2 ? x[g + i + w] : y[i + w];
+                y[i] = fmaxf(upper ? b : a, __shfl_xor_sync(0xffffffffu, upper ? a : b, w));
+            }
+        }
+#pragma unroll
+        for (int w = W; w < 32; w <<= 1) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], w));
+        if (lane < W) out[g + lane] = y[0];
+    }
+}
+
+// The first tile of a segment: its columns' maxima become the references, and
+// the scores (read with references of 0) are taken against them.  A column
+// that sees nothing yet stays unseen.
+template <int C>
+__device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
+{
+    column_max<C>(x, lane, s.red[quad] + c0);
+    any_of(bar, 128, false);
+    if (quad * 32 + lane < C) {
+        const int col = c0 + quad * 32 + lane;
+        const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+        s.neg_m[col] = -fmaxf(top, kUnseen);
+    }
+    any_of(bar, 128, false);
+#pragma unroll
+    for (int i = 0; i < C; i += 4) {
+        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(s.neg_m + c0 + i);
+        unpair(add2(pair(x[i], x[i + 1]), m.x), x[i], x[i + 1]);
+        unpair(add2(pair(x[i + 2], x[i + 3]), m.y), x[i + 2], x[i + 3]);
+    }
+}
+
 
 // This group of four warps gives its columns the maxima of this tile's scores as
 // references where those are higher, and scales its sums and O^T so far.
@@ -549,7 +597,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
 {
     using L = Plan<D, N>;
     // columns of a softmax thread, and those of O it reads at once
-    constexpr int C = L::kCols, CE = C < 16 ? C : 16;
+    constexpr int C = L::kCols, CE = 8;
     constexpr int kSoftWarps = L::kSoftWarps, kSoftThreads = L::kSoftThreads, kLoadWarp = L::kLoadWarp,
                   kMmaWarp = L::kMmaWarp, kQWarp = L::kMmaWarp + 1;
     extern __shared__ uint8_t raw[];
@@ -788,7 +836,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                     s.lse[tid] = (lo + i) * a.q_heads + head;
                 }
                 s.vis[tid] = w;
-                s.neg_m[tid] = -kUnseen;
+                s.neg_m[tid] = 0.f;
                 if (tid == 0) s.bad_v = 0;
             }
             any_of(kAllBar, kSoftThreads, false);
@@ -811,6 +859,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fence_after();
                 float x[C];
                 read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
+                if (t == 0) first_references<C>(s, x, c0, quad, lane, bar);
                 // Two buffers of P: S of this tile was issued after O of the tile before the
                 // last, so once S is there the weights of that tile are done with.
                 if (L::kPBufs == 1 && T > 0) fail = fail || !waitw(smem_addr(&s.pfree[0]), (T - 1) & 1, abort);
