@@ -472,11 +472,11 @@ __device__ __forceinline__ float weigh(float (&x)[C], uint8_t* prow)
 
 // ------------------------------------------------------------ references
 
-// The maxima over a warp's 32 slots of C columns, to out[column].  Halving: each
-// step a lane keeps half of its columns and takes the other lane's maxima of
-// them, C - 1 exchanges in all where one column after the other would take 5 C.
-template <int C>
-__device__ __forceinline__ void column_max(const float (&x)[C], int lane, float* out)
+// C columns of a warp's 32 slots joined by op, to out[column].  Halving: each
+// step a lane keeps half of its columns and takes the other lane's of them, C - 1
+// exchanges in all where one column after the other would take 5 C.
+template <int C, class Op>
+__device__ __forceinline__ void join_columns(const float (&x)[C], int lane, float* out, Op op)
 {
     constexpr int W = C < 32 ? C : 32;
 #pragma unroll
@@ -488,11 +488,11 @@ __device__ __forceinline__ void column_max(const float (&x)[C], int lane, float*
 #pragma unroll
             for (int i = 0; i < w; ++i) {
                 const float a = w == W / 2 ? x[g + i] : y[i], b = w == W / 2 ? x[g + i + w] : y[i + w];
-                y[i] = fmaxf(upper ? b : a, __shfl_xor_sync(0xffffffffu, upper ? a : b, w));
+                y[i] = op(upper ? b : a, __shfl_xor_sync(0xffffffffu, upper ? a : b, w));
             }
         }
 #pragma unroll
-        for (int w = W; w < 32; w <<= 1) y[0] = fmaxf(y[0], __shfl_xor_sync(0xffffffffu, y[0], w));
+        for (int w = W; w < 32; w <<= 1) y[0] = op(y[0], __shfl_xor_sync(0xffffffffu, y[0], w));
         if (lane < W) out[g + lane] = y[0];
     }
 }
@@ -503,7 +503,7 @@ __device__ __forceinline__ void column_max(const float (&x)[C], int lane, float*
 template <int C>
 __device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
 {
-    column_max<C>(x, lane, s.red[quad] + c0);
+    join_columns<C>(x, lane, s.red[quad] + c0, [](float a, float b) { return fmaxf(a, b); });
     any_of(bar, 128, false);
     if (quad * 32 + lane < C) {
         const int col = c0 + quad * 32 + lane;
@@ -885,31 +885,27 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                     for (int e = 0; e < L::kPer; ++e) {
                         const int q = idx + pos_v(t, n) * L::kPer + e, ent = q % L::kRing;
                         fail = fail || !waitw(smem_addr(&s.full[ent]), (q / L::kRing) & 1, abort);
-                        if (slot < len && valid) continue;
+                        if (all || wg >= L::kAtoms) continue;  // one group of warps per atom
                         bool bad = false;
-                        if (wg < L::kAtoms) {  // one group of warps per atom
-                            uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + wg * kTile * 128 + srow * 128);
-                            for (int k = 0; k < 8; ++k) {
-                                if (!valid) {
-                                    v4[k] = make_uint4(0, 0, 0, 0);
-                                    continue;
-                                }
-                                uint4 v = v4[k];
-                                uint32_t* w = reinterpret_cast<uint32_t*>(&v);
-                                bool hit = false;
+                        uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + wg * kTile * 128 + srow * 128);
+                        if (!valid) {
 #pragma unroll
-                                for (int z = 0; z < 4; ++z) {
-                                    if ((w[z] & 0x7F80u) == 0x7F80u) {
-                                        w[z] &= 0xFFFF0000u;
-                                        hit = true;
-                                    }
-                                    if ((w[z] & 0x7F800000u) == 0x7F800000u) {
-                                        w[z] &= 0x0000FFFFu;
-                                        hit = true;
-                                    }
-                                }
-                                if (hit) v4[k] = v;
-                                bad |= hit;
+                            for (int k = 0; k < 8; ++k) v4[k] = make_uint4(0, 0, 0, 0);
+                        } else {
+                            // an exponent of all ones carries into the sign's place
+                            uint32_t ones = 0;
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) {
+                                const uint4 v = v4[k];
+                                ones |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                                        ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+                            }
+                            bad = ones & 0x80008000u;
+                            if (bad) {
+                                uint16_t* h = reinterpret_cast<uint16_t*>(v4);
+#pragma unroll 1
+                                for (int k = 0; k < 64; ++k)
+                                    if ((h[k] & 0x7F80) == 0x7F80) h[k] = 0;
                             }
                         }
                         if (bad) atomicOr(&s.bad_v, 1ull << (slot - len));
@@ -922,20 +918,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             }
             // the columns' sums
             if (!stop) {
+                float sums[C];
 #pragma unroll
-                for (int i = 0; i < C / 2; ++i) {
-                    float v, w;
-                    unpair(l[i], v, w);
-#pragma unroll
-                    for (int o = 16; o > 0; o >>= 1) {
-                        v += __shfl_xor_sync(0xffffffffu, v, o);
-                        w += __shfl_xor_sync(0xffffffffu, w, o);
-                    }
-                    if (lane == 0) {
-                        s.red[quad][c0 + 2 * i] = v;
-                        s.red[quad][c0 + 2 * i + 1] = w;
-                    }
-                }
+                for (int i = 0; i < C / 2; ++i) unpair(l[i], sums[2 * i], sums[2 * i + 1]);
+                join_columns<C>(sums, lane, s.red[quad] + c0, [](float a, float b) { return a + b; });
                 fail = fail || !waitw(smem_addr(&s.ofull), seg & 1, abort);
                 fence_after();
             }
