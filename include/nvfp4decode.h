@@ -358,7 +358,7 @@ NVFP4_API int nvfp4_gemm_grouped(const void* X, int x_per_route, const int32_t* 
  *
  * Limits (else NVFP4_ERR_SHAPE): page_size a power of two in 16..256,
  * head_dim 64, 128 or 256, 1 <= lanes <= NVFP4_CACHE_MAX_LANES, kv_heads <=
- * 256, pages <= 2^24, max_pages <= 2^20 with max_pages * page_size < 2^31,
+ * 256, pages <= 2^24, max_pages <= 2^20 with max_pages * page_size <= 2^30,
  * layers >= 1, pages * kv_heads * page_size < 2^32.  k and v 16-byte aligned,
  * the others 4-byte (NVFP4_ERR_ALIGN); none NULL (NVFP4_ERR_ARG).
  *

@@ -36,7 +36,7 @@ int check_cache(const nvfp4_cache* c)
     const bool dim_ok = c->head_dim == 64 || c->head_dim == 128 || c->head_dim == 256;
     if (!page_ok || !dim_ok || c->lanes < 1 || c->lanes > NVFP4_CACHE_MAX_LANES || c->kv_heads < 1 ||
         c->kv_heads > 256 || c->layers < 1 || c->pages < 1 || c->pages > (1 << 24) || c->max_pages < 1 ||
-        c->max_pages > (1 << 20) || (int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31) ||
+        c->max_pages > (1 << 20) || (int64_t)c->max_pages * c->page_size > ((int64_t)1 << 30) ||
         (int64_t)c->pages * c->kv_heads * c->page_size >= ((int64_t)1 << 32))
         return NVFP4_ERR_SHAPE;
     if (!aligned16(c->k) || !aligned16(c->v)) return NVFP4_ERR_ALIGN;

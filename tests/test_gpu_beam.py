@@ -124,6 +124,35 @@ def test_outputs_may_be_the_inputs_and_workspace_is_left_ready(dev):
     check(dev, x, s, f, ws=ws)
 
 
+def test_two_graphs_at_once(dev):
+    """Two captured selections with a workspace each, replayed on two streams over changing logits."""
+    sets, graphs = [], []
+    for i in range(2):
+        x, s = draw(20 + i, 2, 4, 20000 + i * 3001)
+        ld = -(-x.shape[1] // 4) * 4
+        buf = torch.zeros((8, ld), device=dev)
+        S, ws, st = torch.zeros((2, 4), device=dev), abi.beam_select_workspace(2, 4, x.shape[1], dev), torch.cuda.Stream(dev)
+        st.wait_stream(torch.cuda.current_stream(dev))
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            got = abi.beam_select(buf, S, vocab=x.shape[1], workspace=ws)
+        sets.append((x, s, buf, S, got, st))
+        graphs.append(g)
+    for rnd in range(4):
+        for x, s, buf, S, _, _ in sets:
+            buf[:, :x.shape[1]] = torch.from_numpy(np.roll(x, rnd, 0)).to(dev)
+            S.copy_(torch.from_numpy(s))
+        torch.cuda.synchronize()
+        for _ in range(5):
+            for g, (*_, st) in zip(graphs, sets):
+                with torch.cuda.stream(st):
+                    g.replay()
+        torch.cuda.synchronize()
+        for x, s, _, _, got, _ in sets:
+            _, p, t, _ = cache_ref.beam(np.roll(x, rnd, 0), s.astype(np.float64), None, -1)
+            assert np.array_equal(got[1].cpu().numpy(), p) and np.array_equal(got[2].cpu().numpy(), t)
+
+
 def test_helper_refuses(dev):
     x, s = torch.zeros((4, 100), device=dev), torch.zeros((1, 4), device=dev)
     with pytest.raises(abi.Nvfp4Error) as e:

@@ -189,6 +189,60 @@ def test_draft_and_verify(dev):
     assert not c.ref.any()
 
 
+def test_pools_past_32_bits(dev):
+    """Pools of 4.3 G values: append, attention, fork with copy, compact in pages whose offsets need 64 bits."""
+    pages, hkv, page, D = (1 << 20) + 16, 2, 16, 128
+    k = torch.zeros((1, pages, hkv, page, D), dtype=torch.bfloat16, device=dev)
+    v = torch.zeros_like(k)
+    table = np.full((2, 6), -1, np.int32)
+    table[0, :3] = [pages - 1, pages - 3, pages - 5]
+    table[1, :3] = [pages - 11, pages - 2, pages - 8]
+    ref = torch.ones(pages, dtype=torch.int32, device=dev)  # all taken but two at the far end
+    ref[[pages - 7, pages - 9]] = 0
+    c = abi.Cache(k, v, ch.ints(table, dev), ch.ints([0, 0], dev), ref)
+    counts, f = [40, 37], torch.from_numpy(10000.0 ** (-np.arange(64) / 64)).to(dev)
+    rows = sum(counts)
+    y = torch.randn((rows, (4 + 2 * hkv) * D), generator=torch.Generator(device=dev).manual_seed(1), device=dev)
+    start = ch.ints([0, 40, 77], dev)
+    pos = ch.ints(list(range(40)) + list(range(37)), dev)
+    q = abi.rope_append(c, 0, y, 4, f, pos, row_start=start)
+
+    def small():
+        """The pages in use, renumbered, as the reference."""
+        used = sorted({int(p) for p in c.table.cpu().numpy().ravel() if p >= 0})
+        at = {p: i for i, p in enumerate(used)}
+        idx = torch.tensor(used, device=dev)
+        tab = np.vectorize(lambda p: at.get(int(p), -1))(c.table.cpu().numpy()).astype(np.int32)
+        return cache_ref.RefCache(ch.host_bits(k[:, idx]), ch.host_bits(v[:, idx]), tab, c.len.cpu().numpy(),
+                                  np.ones(len(used), np.int32))
+    r = small()
+    x, _ = cache_ref.rope(y.cpu().numpy(), 4 + 2 * hkv, D, pos.cpu().numpy()[None], np.zeros(64, int), f.cpu().numpy(), 0)
+    for lane, n in enumerate(counts):
+        for i in range(n):
+            p, o = r.where(lane, i)
+            assert np.allclose(cache_ref.bf16_value(r.k[0, p, :, o]), x[40 * lane + i, 4:6], rtol=2.0**-7, atol=1e-4)
+    c.compact(ch.ints(counts, dev))
+    # lane 1 becomes lane 0's twin: its next slot takes a copy of the far last page
+    c.fork(ch.ints([0, 0], dev))
+    c.reserve(ch.ints([4, 4], dev))
+    assert sorted(c.table[:, 2].tolist()) == [pages - 11, pages - 5]  # the lowest page that the fork freed
+    more = torch.randn((8, (4 + 2 * hkv) * D), device=dev)
+    q = abi.rope_append(c, 0, more, 4, f, ch.ints([40, 41, 42, 43] * 2, dev), row_start=ch.ints([0, 4, 8], dev))
+    out, lse = abi.attn_tree(c, 0, q, 0.1, row_start=ch.ints([0, 4, 8], dev), max_nodes=4, want_lse=True)
+    r = small()
+    qh = cache_ref.bf16_value(ch.host_bits(q)).astype(np.float64)
+    want, wl, wabs, err, seen = cache_ref.attention(r, 0, qh, float(np.float32(0.1)), [0, 4, 8], None)
+    tol = wabs * (2 * err[:, :, None] + 2.0**-8 + 2.0**-20) * 1.01 + np.abs(want) * 2.0**-8 * 1.01
+    assert (np.abs(out.float().cpu().numpy() - want) <= tol).all() and (seen == [41, 42, 43, 44] * 2).all()
+    c.compact(ch.ints([2, 1], dev), ch.ints([[1, 3, 0, 0], [2, 0, 0, 0]], dev))
+    r.compact([2, 1], [[1, 3, 0, 0], [2, 0, 0, 0]])
+    s = small()
+    for lane, n in ((0, 42), (1, 41)):
+        for i in range(n):
+            (p, o), (p2, o2) = r.where(lane, i), s.where(lane, i)
+            assert np.array_equal(r.k[0, p, :, o], s.k[0, p2, :, o2]) and np.array_equal(r.v[0, p, :, o], s.v[0, p2, :, o2])
+
+
 FIRST = """
 import sys; sys.path[:0] = ['tests', '.']
 import torch, cache_helpers as ch
