@@ -474,7 +474,7 @@ NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stre
 
 /*
  * Attention of decode rows and drafted trees over the cache, asynchronous (two
- * launches; one where the table holds no more than 128 slots).  Rows and lanes as for nvfp4_rope_append; row r, the i-th of its
+ * launches; one where the table spans few slots).  Rows and lanes as for nvfp4_rope_append; row r, the i-th of its
  * lane b of n rows, sees the lane's committed slots 0 .. len[b] - 1 and those
  * drafted slots len[b] + j, j < n, whose bit j is set in mask[r] (device u64
  * [rows]; a tree: itself and its ancestors).  mask NULL: j <= i, a chain; one

@@ -102,6 +102,7 @@ struct Lanes {
     int base[kMaxLanes + 1];  // first unit of each lane
     int width;                // CTAs that share a (lane, head), one per block of query rows
     int groups;               // of `width` CTAs, that share the units
+    int whole;                // a (lane, cached head) pair is one unit: none is cut
 };
 
 struct Shared {  // at kOffMisc
@@ -127,7 +128,6 @@ struct AttnParams {
     float* part_o;       // [ctas][2][N][D]
     float2* part_ml;     // [ctas][2][N]
     int ctas;            // of the attention kernel
-    int min_tiles;       // tiles a CTA takes at least (but for the last ones)
     int per_block;       // rows of a lane per block: as many whole rows (of G columns) as fit N
     int q_box;           // rows a copy of Q brings (at most per_block)
 };
@@ -356,6 +356,16 @@ __device__ __forceinline__ int range_owner(int units, int groups, int u)
                                : (int)((((int64_t)u + 1) * groups - 1) / units);
 }
 
+// Units of a pair of n tiles.
+__device__ __forceinline__ int units_of(const Lanes& s, int n) { return n == 0 ? 0 : s.whole ? 1 : n + kStart; }
+
+// Cutting pairs and joining their parts costs a call about what kCut tiles do
+// (8 lanes x 8 heads, 8 rows each: 17.8 us cut and 16.0 whole at 800 slots, 19.0
+// and 19.1 at 1,200, 22.1 and 25.1 at 2,000).  So pairs stay whole where the CTAs that get the
+// most of them need no more tiles for it than an even share and kCut.
+constexpr int kCut = 8;
+__host__ __device__ __forceinline__ int turns(int pairs, int width, int ctas) { return (pairs * width + ctas - 1) / ctas; }
+
 // The lanes' rows, lengths and tiles, and the groups, for a whole CTA (two
 // barriers inside; the caller's own follows).
 __device__ __forceinline__ void plan_lanes(const AttnParams& p, Lanes& s, int tid, bool tell)
@@ -386,21 +396,27 @@ __device__ __forceinline__ void plan_lanes(const AttnParams& p, Lanes& s, int ti
         // prefix sums of units and the widest lane, two lanes per thread
         const int lane = tid;
         const int n0 = s.tiles[2 * lane], n1 = s.tiles[2 * lane + 1];
-        const int x0 = n0 ? (n0 + kStart) * c.kv_heads : 0, x1 = n1 ? (n1 + kStart) * c.kv_heads : 0;
-        int incl = x0 + x1, most = max(s.nodes[2 * lane], s.nodes[2 * lane + 1]);
+        const int most = __reduce_max_sync(0xffffffffu, max(s.nodes[2 * lane], s.nodes[2 * lane + 1]));
+        const int longest = __reduce_max_sync(0xffffffffu, max(n0, n1));
+        const int pairs = __reduce_add_sync(0xffffffffu, (n0 > 0) + (n1 > 0)) * c.kv_heads;
+        const int64_t tiles = (int64_t)__reduce_add_sync(0xffffffffu, n0 + n1) * c.kv_heads;
+        const int width = max(1, (most + p.per_block - 1) / p.per_block);
+        const bool whole = (int64_t)turns(pairs, width, p.ctas) * longest <= tiles * width / p.ctas + kCut;
+        const int add = whole ? 0 : kStart;
+        const int x0 = n0 == 0 ? 0 : (whole ? 1 : n0 + add) * c.kv_heads, x1 = n1 == 0 ? 0 : (whole ? 1 : n1 + add) * c.kv_heads;
+        int incl = x0 + x1;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, off);
             if (lane >= off) incl += o;
-            most = max(most, __shfl_xor_sync(0xffffffffu, most, off));
         }
         s.base[2 * lane] = incl - x0 - x1;
         s.base[2 * lane + 1] = incl - x1;
         if (lane == 31) {
             s.base[kMaxLanes] = incl;
-            const int width = max(1, (most + p.per_block - 1) / p.per_block);
             s.width = width;
-            s.groups = min(p.ctas / width, (incl + p.min_tiles - 1) / p.min_tiles);
+            s.whole = whole;
+            s.groups = min(p.ctas / width, incl);
         }
     }
     __syncthreads();
@@ -411,11 +427,16 @@ __device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, 
     Segment g;
     int b = 0;
     while (b + 1 < lanes && s.base[b + 1] <= u) ++b;
-    const int r = u - s.base[b], n = kStart + s.tiles[b];
+    const int r = u - s.base[b], n = units_of(s, s.tiles[b]);
     g.b = b;
     g.h = r / n;
     g.first = s.base[b] + g.h * n;
     g.next = min(g.first + n, u1);
+    if (s.whole) {
+        g.t0 = 0;
+        g.t1 = s.tiles[b];
+        return g;
+    }
     g.t0 = max(u - g.first - kStart, 0);
     g.t1 = g.next - g.first - kStart;  // <= t0: nothing but (a part of) the start
     return g;
@@ -1025,6 +1046,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     if (!(h0 | h1)) return;
     const int b = h0 ? 2 * (__ffs(h0) - 1) : 2 * (__ffs(h1) - 1) + 1;
     const int i = r - s.lo[b], blk = i / p.per_block, col = (i - blk * p.per_block) * G + head % G;
+    if (s.whole) return;
     const int units = s.base[kMaxLanes], first = s.base[b] + head / G * (kStart + s.tiles[b]);
     const int glo = range_owner(units, s.groups, first + kStart),
               ghi = range_owner(units, s.groups, first + kStart + s.tiles[b] - 1);
@@ -1169,8 +1191,11 @@ int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap
         ready.fetch_or(1ull << dev);
     }
     NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)p.ctas), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
-    // a table of one tile cannot be cut
-    if ((int64_t)p.c.max_pages * p.c.page_size > kTile) {
+    // where no pair can be cut, whatever the lengths, there is nothing to join
+    const int lanes = p.c.lanes < p.a.rows ? p.c.lanes : p.a.rows;
+    const int64_t tiles = ((int64_t)p.c.max_pages * p.c.page_size + kTile - 1) / kTile;
+    const int most = turns(lanes * p.c.kv_heads, (p.a.rows + p.per_block - 1) / p.per_block, p.ctas);
+    if (most * tiles > kCut) {
         const unsigned grid = (unsigned)((p.a.rows * p.a.q_heads + 7) / 8);
         NVFP4_CUDA_TRY(launch_pdl(attn_join_kernel<D, N>, dim3(grid), dim3(256), 0, stream, p));
     }
@@ -1229,7 +1254,6 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     AttnParams p;
     p.c = *a->cache;
     p.a = *a;
-    p.min_tiles = 1;
     int sms = 0;
     int st = sm_count(&sms);
     if (st != NVFP4_OK) return st;
