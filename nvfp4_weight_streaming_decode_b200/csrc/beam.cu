@@ -226,7 +226,7 @@ __device__ int block_best(int k, T mine, T none, Above above, Each each, Emit em
     return k;
 }
 
-__global__ void __launch_bounds__(kBeamThreads, 4) beam_kernel(const BeamParams p)
+__global__ void __launch_bounds__(kBeamThreads, kCtasPerSm) beam_kernel(const BeamParams p)
 {
     __shared__ union {
         ListShared<float> f;
