@@ -6,6 +6,11 @@
 // round trip and can be captured in a graph.  There is no free list: a page is
 // free when its reference count is 0, and the lowest free ids are taken first,
 // so the answer does not depend on scheduling.
+//
+// All four are chains of a few small loads and one atomic, 2.5 to 5 us a call,
+// and where slots move, what HBM gives: eight beams' fork and reserve at 64 layers
+// with three copies of 47 slots (74 MB read and written) 19 to 20 us; trim,
+// reserve and compact of eight lanes x 8 drafts at 64 layers 11.6 us.
 #include <cuda_runtime.h>
 #include <stdint.h>
 

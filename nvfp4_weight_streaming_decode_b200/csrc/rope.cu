@@ -7,6 +7,11 @@
 // at position 10^6 a 32-bit product has lost the phase; sine and cosine of the
 // reduced angle are 32-bit.  They are shared by all heads of the row, so a CTA
 // computes the row's table once into shared memory and then streams its heads.
+//
+// Bound by memory for a prompt (8,193 rows of 40 + 2 x 8 heads of 128: 62 us, 5.7
+// TB/s, 0.87 of the measured copy rate), by its chain of small loads for a round
+// (8 rows of 15,360: 3.3 us; 64 rows of 32 heads of 256: 3.5 us).  Each result is
+// rounded to bf16 once, the type the attention's products take.
 #include <cuda_bf16.h>
 #include <cuda_runtime.h>
 #include <stdint.h>
