@@ -465,9 +465,8 @@ def _call(name, device, stream, *args):
     index = device.index
     if stream is None:
         ptr = _current_stream(index)
-    elif stream.device != device:
-        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
     else:
+        _same_device(stream, device)
         ptr = stream.cuda_stream
     fn = getattr(load(), name)
     if torch.cuda.current_device() == index:
@@ -477,6 +476,11 @@ def _call(name, device, stream, *args):
             st = fn(*args, ptr)
     if st != NVFP4_OK:
         check(st, name)
+
+
+def _same_device(stream, device):
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, the tensors on {device}")
 
 
 def _current_stream(index):
@@ -596,6 +600,7 @@ def rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis=None, s
     [rot_dim / 2]; row_start: int32 [lanes + 1], or None for one row per lane."""
     if stream is not None:  # what is allocated here belongs to the stream that uses it
         import torch
+        _same_device(stream, cache.device)
         with torch.cuda.stream(stream):
             return rope_append(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
     a, q = _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, row_start, q)
@@ -656,6 +661,7 @@ def attn_tree(cache, layer, q, scale, row_start=None, mask=None, max_nodes=1, ou
     attn_tree_workspace, one for each stream or graph whose calls may overlap (None: a new one)."""
     if stream is not None:  # what is allocated here belongs to the stream that uses it
         import torch
+        _same_device(stream, cache.device)
         with torch.cuda.stream(stream):
             return attn_tree(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse, workspace)
     a, out, lse, workspace = _attn_record(cache, layer, q, scale, row_start, mask, max_nodes, out, want_lse, lse,
@@ -681,6 +687,7 @@ def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=No
     [groups][beams] with its end token eos; parent is the row of logits that is extended (what Cache.fork takes)."""
     import torch
     if stream is not None:  # what is allocated here belongs to the stream that uses it
+        _same_device(stream, logits.device)
         with torch.cuda.stream(stream):
             return beam_select(logits, scores, vocab, finished, eos, scores_out, parent, token, finished_out, workspace)
     dev = logits.device

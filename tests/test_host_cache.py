@@ -2,6 +2,7 @@
 status before the library touches CUDA.  And of the 64-bit references
 themselves on hand-worked cases."""
 import ctypes
+import types
 
 import numpy as np
 import pytest
@@ -210,6 +211,17 @@ def tiny():
     k = np.arange(1 * 4 * 1 * 16 * 2, dtype=np.uint16).reshape(1, 4, 1, 16, 2)
     table = np.array([[2, -1], [0, -1]], np.int32)
     return cache_ref.RefCache(k, k + 1000, table, np.array([3, 2], np.int32), np.array([1, 0, 1, 0], np.int32))
+
+
+def test_helpers_refuse_a_stream_of_another_device():
+    torch = pytest.importorskip("torch")
+    here, there = torch.device("cuda", 0), types.SimpleNamespace(device=torch.device("cuda", 1))
+    on = types.SimpleNamespace(device=here)  # of the tensors, no more than their device is looked at
+    for call in (lambda: abi.rope_append(on, 0, None, 8, None, None, stream=there),
+                 lambda: abi.attn_tree(on, 0, None, 1.0, stream=there),
+                 lambda: abi.beam_select(on, None, stream=there)):
+        with pytest.raises(ValueError, match="stream is on cuda:1"):
+            call()
 
 
 def test_reference_fork_reserve_compact_trim():
