@@ -79,12 +79,15 @@ constexpr uint32_t kPolls = 1u << 20;      // about a second
 
 // Shared-memory plan of a variant.  The ring's entries are 128 slots x up to
 // 128 values of K or V, as atoms of 128 slots x 64 values (128 bytes a slot).
+// N = 256: two halves of 128 query rows as the products' rows (attn_wide_kernel).
 template <int D, int N>
 struct Plan {
+    static constexpr bool kWide = N == 256;
+    static constexpr int kD = D, kN = N;
     static constexpr int kAtoms = D >= 128 ? 2 : 1;          // atoms per ring entry
     static constexpr int kEntry = kAtoms * kTile * 128;      // bytes
     static constexpr int kPer = D > 128 ? 2 : 1;             // entries per tile of K (or V)
-    static constexpr int kPBufs = N == 128 && D == 256 ? 1 : 2;
+    static constexpr int kPBufs = kWide ? 0 : N == 128 && D == 256 ? 1 : 2;
     static constexpr int kPBytes = kTile * N * 2;
     static constexpr int kQBytes = N * D * 2;
     static constexpr int kBudget = 226 * 1024 - 8192;        // what is left holds barriers and the lane tables
@@ -94,7 +97,7 @@ struct Plan {
     static constexpr int kOffQ = kOffP + kPBufs * kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     // Softmax warps come in two groups of four (32 slots each), half the columns each.
-    static constexpr int kCols = N / 2;                      // columns per softmax thread
+    static constexpr int kCols = kWide ? kTile : N / 2;      // columns per softmax thread
     static constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
     static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
     static constexpr int kThreads = kSoftThreads + 128;      // the last group: pages, products, queries, an idle warp
@@ -105,7 +108,7 @@ struct Plan {
     static constexpr int kOBlocks = D > 128 ? 2 : 1;         // 128-row blocks of O^T
     // loads and products take entries in one order, so a tile of V beside one entry of K is enough to go on
     static_assert(kRing > kPer, "V of a tile fits the ring");
-    static_assert(2 * N + kOBlocks * N <= 512, "tensor memory");
+    static_assert(kWide ? D <= 128 : 2 * N + kOBlocks * N <= 512, "tensor memory");
 };
 
 // What the schedule goes by.
@@ -117,10 +120,13 @@ struct Lanes {
     int whole;                // a (lane, cached head) pair is one unit: none is cut
 };
 
+constexpr int kCleaned = 8;  // more than the tiles of V a ring holds
+
 struct Shared {  // at kOffMisc
     uint64_t full[12], empty[12];
     uint64_t sfull[2], pfull[2], pfree[2];
     uint64_t qfull, qempty, ofull, drain;
+    uint64_t cleaned[kCleaned], odone[2], left[2];  // of attn_wide_kernel
     uint32_t tmem;
     int abort;
     unsigned long long bad_v;          // drafted slots with non-finite values, this segment
@@ -180,6 +186,16 @@ __device__ __forceinline__ void mma(uint32_t leader, uint32_t d, uint64_t a, uin
         "l"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader), "r"(0u)
         : "memory");
 }
+// The same with A in tensor memory: a row's values in pairs, 16 of them in 8 columns.
+__device__ __forceinline__ void mma_tm(uint32_t leader, uint32_t d, uint32_t a, uint64_t b, uint32_t idesc,
+                                       uint32_t accumulate)
+{
+    asm volatile(
+        "{\n .reg .pred p, e;\n setp.ne.b32 p, %4, 0;\n setp.ne.b32 e, %5, 0;\n"
+        " @e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, {%6, %6, %6, %6}, p;\n}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate), "r"(leader), "r"(0u)
+        : "memory");
+}
 __device__ __forceinline__ void commit(uint32_t leader, uint32_t bar)
 {
     asm volatile(
@@ -224,8 +240,24 @@ __device__ __forceinline__ void tm_st8(uint32_t t, const float* v)
                  "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                  : "memory");
 }
+__device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(t),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
 __device__ __forceinline__ void tm_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void tm_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// After tm_wait_ld: what was loaded is not used before this.
+template <int C>
+__device__ __forceinline__ void settled(float (&v)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C; ++i) asm volatile("" : "+f"(v[i]));
+}
 
 template <int C>
 __device__ __forceinline__ void tm_ld(uint32_t t, float (&v)[C])
@@ -237,6 +269,7 @@ __device__ __forceinline__ void tm_ld(uint32_t t, float (&v)[C])
         for (int i = 0; i < C; i += 16) tm_ld16(t + i, v + i);
     }
     tm_wait_ld();
+    settled(v);
 }
 
 __device__ __forceinline__ void tma_page(uint32_t dst, const CUtensorMap* map, int x, int row, int head, int page,
@@ -503,6 +536,25 @@ __device__ __forceinline__ float weigh(float (&x)[C], uint8_t* prow)
     return over;
 }
 
+// Zero for the NaN and infinities of 64 bf16 values; whether there were any.
+__device__ __forceinline__ bool drop_non_finite(uint4* v4)
+{
+    // an exponent of all ones carries into the sign's place
+    uint32_t ones = 0;
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+        const uint4 v = v4[k];
+        ones |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
+                ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
+    }
+    if (!(ones & 0x80008000u)) return false;
+    uint16_t* h = reinterpret_cast<uint16_t*>(v4);
+#pragma unroll 1
+    for (int k = 0; k < 64; ++k)
+        if ((h[k] & 0x7F80) == 0x7F80) h[k] = 0;
+    return true;
+}
+
 // ------------------------------------------------------------ references
 
 // C columns of a warp's 32 slots joined by op, to out[column].  Halving: each
@@ -565,8 +617,7 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
 #pragma unroll 1
     for (int i0 = 0; i0 < C; i0 += 8) {
         float x[8];
-        tm_ld8(at_s + i0, x);
-        tm_wait_ld();
+        tm_ld(at_s + i0, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             float v = plain || all || (s.vis[c0 + i0 + i] & bit) ? x[i] * sl : -INFINITY;
@@ -603,8 +654,7 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
             for (int blkd = 0; blkd < L::kOBlocks; ++blkd) {
                 float o[8];
                 const uint32_t at = at_o + blkd * N + i0;
-                tm_ld8(at, o);
-                tm_wait_ld();
+                tm_ld(at, o);
 #pragma unroll
                 for (int j = 0; j < 8; ++j) o[j] *= down[j];
                 tm_st8(at, o);
@@ -619,6 +669,154 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
         s.neg_m[col] = -fmaxf(-s.neg_m[col], fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
                                                    fmaxf(s.red[2][col], s.red[3][col])));
     any_of(bar, 128, false);
+}
+
+// ------------------------------------------------- what both kernels share
+
+// Barriers, tensor memory, the schedule (for a whole CTA; ends with a barrier).
+template <class L>
+__device__ __forceinline__ void start_cta(const AttnParams& p, Shared& s, uint8_t* sm, const CUtensorMap& map_k,
+                                          const CUtensorMap& map_v, const CUtensorMap& map_q)
+{
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    if (tid == 0) {
+        for (int i = 0; i < 12; ++i) {
+            mbar_init(smem_addr(&s.full[i]), 1);
+            mbar_init(smem_addr(&s.empty[i]), 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(smem_addr(&s.sfull[i]), 1);
+            mbar_init(smem_addr(&s.pfull[i]), L::kWide ? 4 : L::kSoftWarps);
+            mbar_init(smem_addr(&s.pfree[i]), 1);
+        }
+        mbar_init(smem_addr(&s.qfull), 1);
+        mbar_init(smem_addr(&s.qempty), 1);
+        mbar_init(smem_addr(&s.ofull), 1);
+        mbar_init(smem_addr(&s.drain), 1);
+        if (L::kWide) {
+            for (int i = 0; i < kCleaned; ++i) mbar_init(smem_addr(&s.cleaned[i]), 1);
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(smem_addr(&s.odone[i]), 1);
+                mbar_init(smem_addr(&s.left[i]), 4);
+            }
+        }
+        s.abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == L::kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    if (warp == L::kLoadWarp && lane == 0) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
+    }
+    // columns of Q that no copy writes stay zero
+    for (int i = tid; i < L::kQBytes / 16; i += L::kThreads)
+        *reinterpret_cast<uint4*>(sm + L::kOffQ + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_async();
+    // The join may start once what came before this kernel is complete: it then
+    // reads row ranges and lengths while this one runs out.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    plan_lanes(p, s.lanes, tid, blockIdx.x == 0);
+    fence_after();
+    __syncthreads();
+}
+
+// A warp: pages -> ring, in the order K0, K1, V0, K2, V1, ...
+template <class L>
+__device__ __forceinline__ void load_pages(const AttnParams& p, Shared& s, uint32_t ring, const CUtensorMap& map_k,
+                                           const CUtensorMap& map_v, int u0, int u1, int blk, int lane)
+{
+    const nvfp4_cache& c = p.c;
+    const int shift = __ffs(c.page_size) - 1;
+    volatile int* abort = &s.abort;
+    int idx = 0;  // entries issued so far
+    int done = 0;
+    bool ok = true;
+    const int box = min(c.page_size, kTile);         // slots per copy
+    const int pieces = kTile / box;                  // copies per atom of a tile
+    for (int u = u0; ok && u < u1;) {
+        const Segment g = segment_at(s.lanes, c.lanes, u, u1);
+        u = g.next;
+        if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+        const int n = g.t1 - g.t0;
+        const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
+        const int end = s.lanes.end[g.b];
+        // lane i < pieces holds the page of piece i; one tile ahead for K
+        auto page_of = [&](int t) {
+            const int slot = (g.t0 + t) * kTile + lane * box;
+            return lane < pieces && slot < end ? row[slot >> shift] : -1;
+        };
+        auto fetch = [&](const CUtensorMap* map, int pg, int t, int pos) {
+            const bool good = pg >= 0 && pg < c.pages;
+            const unsigned have = __ballot_sync(0xffffffffu, good);
+            const int off = ((g.t0 + t) * kTile + lane * box) & (c.page_size - 1);
+            for (int e = 0; e < L::kPer; ++e) {
+                const int q = idx + pos * L::kPer + e, slot = q % L::kRing;
+                if (q >= L::kRing && !waitw(smem_addr(&s.empty[slot]), ((q / L::kRing) - 1) & 1, abort)) return false;
+                const uint32_t bar = smem_addr(&s.full[slot]);
+                if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(have) * L::kAtoms * box * 128));
+                __syncwarp();
+                if (good) {
+                    const uint32_t dst = ring + slot * L::kEntry + lane * box * 128;
+#pragma unroll
+                    for (int x = 0; x < L::kAtoms; ++x)
+                        tma_page(dst + x * kTile * 128, map, e * 128 + x * 64, off, g.h, pg, bar);
+                }
+                done = q + 1;
+            }
+            return true;
+        };
+        int prev = page_of(0), next = n > 1 ? page_of(1) : -1;
+        ok = fetch(&map_k, prev, 0, 0);
+        for (int t = 1; ok && t < n; ++t) {
+            const int cur = next;
+            if (t + 1 < n) next = page_of(t + 1);
+            ok = fetch(&map_k, cur, t, pos_k(t)) && fetch(&map_v, prev, t - 1, pos_v(t - 1, n));
+            prev = cur;
+        }
+        ok = ok && fetch(&map_v, prev, n - 1, pos_v(n - 1, n));
+        idx += 2 * n * L::kPer;
+    }
+    if (!ok && lane == 0) give_up(abort);
+    // nothing in flight when the CTA ends: the last ring's worth of entries
+    for (int q = max(0, done - L::kRing); q < done; ++q)
+        warp_wait(smem_addr(&s.full[q % L::kRing]), (q / L::kRing) & 1);
+}
+
+// A warp: the block's rows x the pair's G heads, as the columns' order wants them.
+template <class L>
+__device__ __forceinline__ void load_queries(const AttnParams& p, Shared& s, uint32_t qbuf, const CUtensorMap& map_q,
+                                             int u0, int u1, int blk, int lane)
+{
+    const nvfp4_cache& c = p.c;
+    const int G = p.a.q_heads / c.kv_heads;
+    volatile int* abort = &s.abort;
+    int seg = 0;
+    bool ok = true;
+    for (int u = u0; ok && u < u1;) {
+        const Segment g = segment_at(s.lanes, c.lanes, u, u1);
+        u = g.next;
+        if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+        if (seg > 0) ok = waitw(smem_addr(&s.qempty), (seg - 1) & 1, abort);
+        if (ok && lane == 0) {
+            const uint32_t bar = smem_addr(&s.qfull);
+            mbar_expect_tx(bar, (uint32_t)(p.q_box * G * L::kD * 2));
+            for (int x = 0; x < L::kD / 64; ++x)
+                tma_rows(qbuf + x * L::kN * 128, &map_q, x * 64, g.h * G, s.lanes.lo[g.b] + blk * p.per_block, bar);
+        }
+        __syncwarp();
+        ++seg;
+    }
+    if (seg > 0) {
+        if (!ok && lane == 0) give_up(abort);
+        warp_wait(smem_addr(&s.qfull), (seg - (ok ? 1 : 2)) & 1);  // the last copy has landed
+    }
 }
 
 // ---------------------------------------------------------------- the kernel
@@ -645,45 +843,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
     const int shift = __ffs(c.page_size) - 1;
     volatile int* abort = &s.abort;
 
-    if (tid == 0) {
-        for (int i = 0; i < 12; ++i) {
-            mbar_init(smem_addr(&s.full[i]), 1);
-            mbar_init(smem_addr(&s.empty[i]), 1);
-        }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(smem_addr(&s.sfull[i]), 1);
-            mbar_init(smem_addr(&s.pfull[i]), kSoftWarps);
-            mbar_init(smem_addr(&s.pfree[i]), 1);
-        }
-        mbar_init(smem_addr(&s.qfull), 1);
-        mbar_init(smem_addr(&s.qempty), 1);
-        mbar_init(smem_addr(&s.ofull), 1);
-        mbar_init(smem_addr(&s.drain), 1);
-        s.abort = 0;
-        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
-    }
-    if (warp == kMmaWarp) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&s.tmem))
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-        fence_before();
-    }
-    if (warp == kLoadWarp && lane == 0) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_k) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_v) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&map_q) : "memory");
-    }
-    // columns of Q that no copy writes stay zero
-    for (int i = tid; i < L::kQBytes / 16; i += L::kThreads)
-        *reinterpret_cast<uint4*>(sm + L::kOffQ + i * 16) = make_uint4(0, 0, 0, 0);
-    fence_async();
-    // The join may start once what came before this kernel is complete: it then
-    // reads row ranges and lengths while this one runs out.
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    plan_lanes(p, s.lanes, tid, blockIdx.x == 0);
-    fence_after();
-    __syncthreads();
+    start_cta<L>(p, s, sm, map_k, map_v, map_q);
     const uint32_t tmem = s.tmem;
     const uint32_t tm_s = tmem, tm_o = tmem + 2 * N;
     // this CTA's range and its block of query rows
@@ -694,83 +854,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
 
     if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRest));
     if (warp == kLoadWarp) {
-        // ---- pages -> ring
-        int idx = 0;  // entries issued so far
-        int done = 0;
-        bool ok = true;
-        const int box = min(c.page_size, kTile);         // slots per copy
-        const int pieces = kTile / box;                  // copies per atom of a tile
-        for (int u = u0; ok && u < u1;) {
-            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u = g.next;
-            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
-            const int n = g.t1 - g.t0;
-            const int32_t* row = c.table + (int64_t)g.b * c.max_pages;
-            const int end = s.lanes.end[g.b];
-            // lane i < pieces holds the page of piece i; one tile ahead for K
-            auto page_of = [&](int t) {
-                const int slot = (g.t0 + t) * kTile + lane * box;
-                return lane < pieces && slot < end ? row[slot >> shift] : -1;
-            };
-            auto fetch = [&](const CUtensorMap* map, int pg, int t, int pos) {
-                const bool good = pg >= 0 && pg < c.pages;
-                const unsigned have = __ballot_sync(0xffffffffu, good);
-                const int off = ((g.t0 + t) * kTile + lane * box) & (c.page_size - 1);
-                for (int e = 0; e < L::kPer; ++e) {
-                    const int q = idx + pos * L::kPer + e, slot = q % L::kRing;
-                    if (q >= L::kRing && !waitw(smem_addr(&s.empty[slot]), ((q / L::kRing) - 1) & 1, abort)) return false;
-                    const uint32_t bar = smem_addr(&s.full[slot]);
-                    if (lane == 0) mbar_expect_tx(bar, (uint32_t)(__popc(have) * L::kAtoms * box * 128));
-                    __syncwarp();
-                    if (good) {
-                        const uint32_t dst = ring + slot * L::kEntry + lane * box * 128;
-#pragma unroll
-                        for (int x = 0; x < L::kAtoms; ++x)
-                            tma_page(dst + x * kTile * 128, map, e * 128 + x * 64, off, g.h, pg, bar);
-                    }
-                    done = q + 1;
-                }
-                return true;
-            };
-            int prev = page_of(0), next = n > 1 ? page_of(1) : -1;
-            ok = fetch(&map_k, prev, 0, 0);
-            for (int t = 1; ok && t < n; ++t) {
-                const int cur = next;
-                if (t + 1 < n) next = page_of(t + 1);
-                ok = fetch(&map_k, cur, t, pos_k(t)) && fetch(&map_v, prev, t - 1, pos_v(t - 1, n));
-                prev = cur;
-            }
-            ok = ok && fetch(&map_v, prev, n - 1, pos_v(n - 1, n));
-            idx += 2 * n * L::kPer;
-        }
-        if (!ok) {
-            if (lane == 0) give_up(abort);
-            // copies in flight: the last ring's worth of entries
-            for (int q = max(0, done - L::kRing); q < done; ++q)
-                warp_wait(smem_addr(&s.full[q % L::kRing]), (q / L::kRing) & 1);
-        }
+        load_pages<L>(p, s, ring, map_k, map_v, u0, u1, blk, lane);
     } else if (warp == kQWarp) {
-        // ---- queries: the block's rows x the pair's G heads, as the columns' order wants them
-        int seg = 0;
-        bool ok = true;
-        for (int u = u0; ok && u < u1;) {
-            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
-            u = g.next;
-            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
-            if (seg > 0) ok = waitw(smem_addr(&s.qempty), (seg - 1) & 1, abort);
-            if (ok && lane == 0) {
-                const uint32_t bar = smem_addr(&s.qfull);
-                mbar_expect_tx(bar, (uint32_t)(p.q_box * G * D * 2));
-                for (int x = 0; x < D / 64; ++x)
-                    tma_rows(qbuf + x * N * 128, &map_q, x * 64, g.h * G, s.lanes.lo[g.b] + blk * p.per_block, bar);
-            }
-            __syncwarp();
-            ++seg;
-        }
-        if (seg > 0) {
-            if (!ok && lane == 0) give_up(abort);
-            warp_wait(smem_addr(&s.qfull), (seg - (ok ? 1 : 2)) & 1);  // the last copy has landed
-        }
+        load_queries<L>(p, s, qbuf, map_q, u0, u1, blk, lane);
     } else if (warp == kMmaWarp) {
         // ---- the products
         const uint32_t lead = elect();
@@ -834,11 +920,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             done += n;
             ++seg;
         }
-        if (!ok) {
-            if (lane == 0) give_up(abort);
-            commit(lead, smem_addr(&s.drain));  // products in flight (a wait that the abort does not cut short)
-            warp_wait(smem_addr(&s.drain), 0);
-        }
+        if (!ok && lane == 0) give_up(abort);
+        commit(lead, smem_addr(&s.drain));  // products in flight (a wait that the abort does not cut short)
+        warp_wait(smem_addr(&s.drain), 0);
     } else if (warp < kSoftWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoft));
         // ---- softmax: thread = slot (and value row of O^T), half the columns
@@ -925,21 +1009,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
 #pragma unroll
                             for (int k = 0; k < 8; ++k) v4[k] = make_uint4(0, 0, 0, 0);
                         } else {
-                            // an exponent of all ones carries into the sign's place
-                            uint32_t ones = 0;
-#pragma unroll
-                            for (int k = 0; k < 8; ++k) {
-                                const uint4 v = v4[k];
-                                ones |= ((v.x & 0x7F807F80u) + 0x00800080u) | ((v.y & 0x7F807F80u) + 0x00800080u) |
-                                        ((v.z & 0x7F807F80u) + 0x00800080u) | ((v.w & 0x7F807F80u) + 0x00800080u);
-                            }
-                            bad = ones & 0x80008000u;
-                            if (bad) {
-                                uint16_t* h = reinterpret_cast<uint16_t*>(v4);
-#pragma unroll 1
-                                for (int k = 0; k < 64; ++k)
-                                    if ((h[k] & 0x7F80) == 0x7F80) h[k] = 0;
-                            }
+                            bad = drop_non_finite(v4);
                         }
                         if (bad) atomicOr(&s.bad_v, 1ull << (slot - len));
                     }
@@ -1022,6 +1092,405 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             ++seg;
         }
         if (fail && lane == 0) give_up(abort);
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        fence_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// ---------------------------------------------------- many rows to a head
+
+// 128 log2 scores of a row, 32 at a time with the next ones on their way: f(i,
+// x) gets those from slot i on, x = s scale log2(e) + neg_m, masked ones -inf.
+// `plain`: every slot is seen.
+template <class F>
+__device__ __forceinline__ void row_scores(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[4], F f)
+{
+    const f32x2 scale = pair(sl, sl), minus = pair(neg_m, neg_m);
+    float x[2][32];
+    tm_ld16(at, x[0]);
+    tm_ld16(at + 16, x[0] + 16);
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        float(&y)[32] = x[c & 1];
+        tm_wait_ld();
+        settled(y);
+        if (c < 3) {
+            tm_ld16(at + 32 * (c + 1), x[(c + 1) & 1]);
+            tm_ld16(at + 32 * (c + 1) + 16, x[(c + 1) & 1] + 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) unpair(fma2(pair(y[i], y[i + 1]), scale, minus), y[i], y[i + 1]);
+        if (!plain) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i)
+                if (!(seen[c] >> i & 1)) y[i] = -INFINITY;
+        }
+        f(32 * c, y);
+    }
+}
+
+// The largest of a row's 128 log2 scores.
+__device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, const uint32_t (&seen)[4])
+{
+    float top = -INFINITY;
+    row_scores(at, sl, 0.f, plain, seen, [&](int, const float (&x)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
+    });
+    return top;
+}
+
+// A row's weights as packed bf16 pairs, and their sum (of the weights before
+// their rounding); returns the largest log2 weight.
+__device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[4],
+                                           uint32_t (&w)[kTile / 2], float& sum)
+{
+    float over = -INFINITY;
+    f32x2 s0 = 0, s1 = 0;
+    row_scores(at, sl, neg_m, plain, seen, [&](int i0, float (&x)[32]) {
+#pragma unroll
+        for (int i = 0; i < 32; i += 4) {
+            over = max3(over, x[i], x[i + 1]);
+            over = max3(over, x[i + 2], x[i + 3]);
+#pragma unroll
+            for (int j = i; j < i + 4; ++j) x[j] = fast_exp2(x[j]);
+            s0 = add2(s0, pair(x[i], x[i + 1]));
+            s1 = add2(s1, pair(x[i + 2], x[i + 3]));
+#pragma unroll
+            for (int j = i; j < i + 4; j += 2) {
+                const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], x[j + 1]);
+                w[(i0 + j) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+            }
+        }
+    });
+    float a, b, c, d;
+    unpair(s0, a, b);
+    unpair(s1, c, d);
+    sum = (a + b) + (c + d);
+    return over;
+}
+
+// For lanes with more than 128 query rows to a cached head.  The rows are the
+// products' rows here,
+//     S [128 rows][128 slots] = Q K^T,   O [128 rows][D] += P V
+// so a thread owns a row: no maximum or sum crosses threads, and P goes back to
+// tensor memory, over the scores it came from, which takes its 32 KB (written
+// and read) out of the shared memory's way.  A CTA has two halves of 128 rows, four warps
+// each, that take turns: while one half's warps form weights, the tensor cores
+// work for the other.  V is shared, so one more warp looks after its slots that
+// rows must not see, ahead of the products.
+template <int D>
+__global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
+    attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
+                     const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
+{
+    using L = Plan<D, 256>;
+    constexpr int kHalf = 128, kSoftWarps = L::kSoftWarps, kLoadWarp = L::kLoadWarp, kMmaWarp = L::kMmaWarp,
+                  kQWarp = L::kMmaWarp + 1;
+    extern __shared__ uint8_t raw[];
+    uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
+    Shared& s = *reinterpret_cast<Shared*>(sm + L::kOffMisc);
+    const uint32_t ring = smem_addr(sm), qbuf = ring + L::kOffQ;
+    const nvfp4_cache& c = p.c;
+    const nvfp4_attn_args& a = p.a;
+    const int tid = threadIdx.x, lane = tid & 31;
+    const int warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
+    const int G = a.q_heads / c.kv_heads;
+    const int shift = __ffs(c.page_size) - 1;
+    volatile int* abort = &s.abort;
+
+    start_cta<L>(p, s, sm, map_k, map_v, map_q);
+    const uint32_t tmem = s.tmem;
+    const uint32_t tm_s = tmem, tm_o = tmem + 2 * kTile;  // [half][128 columns] each
+    const int units = s.lanes.base[kMaxLanes], width = s.lanes.width, groups = s.lanes.groups;
+    const int group = blockIdx.x / width, blk = blockIdx.x % width;
+    const bool idle = group >= groups;
+    const int u0 = idle ? 0 : range_begin(units, groups, group), u1 = idle ? 0 : range_begin(units, groups, group + 1);
+
+    if (warp >= kSoftWarps) asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(L::kRest));
+    if (warp == kLoadWarp) {
+        load_pages<L>(p, s, ring, map_k, map_v, u0, u1, blk, lane);
+    } else if (warp == kQWarp) {
+        load_queries<L>(p, s, qbuf, map_q, u0, u1, blk, lane);
+    } else if (warp == kMmaWarp) {
+        // ---- the products
+        const uint32_t lead = elect();
+        constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
+        constexpr uint32_t kIdS = kBase | ((uint32_t)(kTile >> 3) << 17);
+        constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
+        int idx = 0, seg = 0, tiles = 0;
+        int did[2] = {0, 0};  // tiles of earlier segments, per half
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            const int halves = min(p.per_block, s.lanes.nodes[g.b] - blk * p.per_block) * G > kHalf ? 2 : 1;
+            ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
+            // S of a tile, over the weights of the tile before
+            auto scores = [&](int t, int w) {
+                const int q = idx + pos_k(t), slot = q % L::kRing, T = did[w] + t;
+                if (w == 0 && !waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort)) return false;
+                if (T > 0 && !waitw(smem_addr(&s.pfree[w]), (T - 1) & 1, abort)) return false;
+                fence_after();
+#pragma unroll
+                for (int x = 0; x < L::kAtoms; ++x)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        mma(lead, tm_s + w * kTile, desc_k(qbuf + x * 256 * 128 + w * kHalf * 128 + k * 32),
+                            desc_k(ring + slot * L::kEntry + x * kTile * 128 + k * 32), kIdS, (x | k) != 0);
+                commit(lead, smem_addr(&s.sfull[w]));
+                if (w == halves - 1) {
+                    commit(lead, smem_addr(&s.empty[slot]));
+                    if (t == n - 1) commit(lead, smem_addr(&s.qempty));
+                }
+                return true;
+            };
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (w < halves) ok = ok && scores(0, w);
+            for (int t = 0; ok && t < n; ++t) {
+                const int q = idx + pos_v(t, n), slot = q % L::kRing, V = tiles + t;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    if (w >= halves || !ok) continue;
+                    if (w == 0)
+                        ok = waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort) &&
+                             waitw(smem_addr(&s.cleaned[V % kCleaned]), (V / kCleaned) & 1, abort);
+                    ok = ok && waitw(smem_addr(&s.pfull[w]), (did[w] + t) & 1, abort);
+                    if (!ok) continue;
+                    fence_after();
+#pragma unroll
+                    for (int k = 0; k < kTile / 16; ++k)
+                        mma_tm(lead, tm_o + w * kHalf, tm_s + w * kTile + 8 * k,
+                               desc_mn(ring + slot * L::kEntry + k * 2048, L::kAtoms == 2 ? kTile * 128 : 0), kIdO,
+                               t > 0 || k != 0);
+                    commit(lead, smem_addr(&s.pfree[w]));
+                    if (w == halves - 1) commit(lead, smem_addr(&s.empty[slot]));
+                    if (t == n - 1)
+                        commit(lead, smem_addr(&s.odone[w]));
+                    else
+                        ok = scores(t + 1, w);
+                }
+            }
+            idx += 2 * n;
+            tiles += n;
+            did[0] += n;
+            if (halves == 2) did[1] += n;
+            ++seg;
+        }
+        if (!ok && lane == 0) give_up(abort);
+        commit(lead, smem_addr(&s.drain));
+        warp_wait(smem_addr(&s.drain), 0);
+    } else if (warp == kQWarp + 1) {
+        // ---- V's rows behind the last slot or of a bad page become zero, and the
+        // non-finite values of drafted slots too; a lane looks at four slots
+        int idx = 0, tiles = 0;
+        int segs[2] = {0, 0};  // earlier segments, per half
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            const int len = s.lanes.len[g.b], end = s.lanes.end[g.b];
+            const int32_t* trow = c.table + (int64_t)g.b * c.max_pages;
+            // the results of the segments before are out: bad_v is free
+#pragma unroll
+            for (int w = 0; w < 2; ++w)
+                if (segs[w] > 0) ok = ok && waitw(smem_addr(&s.left[w]), (segs[w] - 1) & 1, abort);
+            if (lane == 0) s.bad_v = 0;
+            __syncwarp();
+            for (int t = 0; ok && t < n; ++t) {
+                const int q = idx + pos_v(t, n), ent = q % L::kRing, V = tiles + t;
+                const int slot0 = (g.t0 + t) * kTile + lane;
+                unsigned good = 0, all = 0;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int slot = slot0 + 32 * z;
+                    const int pg = slot < end ? trow[slot >> shift] : -1;
+                    const bool valid = slot < end && pg >= 0 && pg < c.pages;
+                    if (slot < end && !valid) atomicOr(&g_attn_status, kBadPage);
+                    good |= valid ? 1u << z : 0u;
+                    all |= valid && slot < len ? 1u << z : 0u;
+                }
+                ok = waitw(smem_addr(&s.full[ent]), (q / L::kRing) & 1, abort);
+                if (!ok) break;
+                if (__any_sync(0xffffffffu, all != 15u)) {
+#pragma unroll 1
+                    for (int z = 0; z < 4 * L::kAtoms; ++z) {
+                        const int zs = z / L::kAtoms, slot = slot0 + 32 * zs;
+                        if (all >> zs & 1) continue;
+                        uint4* v4 = reinterpret_cast<uint4*>(sm + ent * L::kEntry + z % L::kAtoms * kTile * 128 +
+                                                             (lane + 32 * zs) * 128);
+                        if (!(good >> zs & 1)) {
+#pragma unroll
+                            for (int k = 0; k < 8; ++k) v4[k] = make_uint4(0, 0, 0, 0);
+                        } else if (drop_non_finite(v4)) {
+                            atomicOr(&s.bad_v, 1ull << (slot - len));
+                        }
+                    }
+                    fence_async();
+                    __syncwarp();
+                }
+                if (lane == 0) mbar_arrive(smem_addr(&s.cleaned[V % kCleaned]));
+            }
+            idx += 2 * n;
+            tiles += n;
+            ++segs[0];
+            if (min(p.per_block, s.lanes.nodes[g.b] - blk * p.per_block) * G > kHalf) ++segs[1];
+        }
+        if (!ok && lane == 0) give_up(abort);
+    } else if (warp < kSoftWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(L::kSoft));
+        // ---- softmax: thread = row
+        const int half = warp >> 2, quad = warp & 3, col = half * kHalf + quad * 32 + lane;
+        const uint32_t lanebits = (uint32_t)(quad * 32) << 16;
+        const uint32_t at_s = tm_s + half * kTile + lanebits, at_o = tm_o + half * kHalf + lanebits;
+        const float sl = a.scale * 1.4426950408889634f;
+        int seg = 0, did = 0, tiles = 0;
+        bool ok = true;
+        for (int u = u0; ok && u < u1;) {
+            const Segment g = segment_at(s.lanes, c.lanes, u, u1);
+            u = g.next;
+            if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
+            const int n = g.t1 - g.t0;
+            const int len = s.lanes.len[g.b], end = s.lanes.end[g.b], lo = s.lanes.lo[g.b], nodes = s.lanes.nodes[g.b];
+            const int rows = min(p.per_block, nodes - blk * p.per_block) * G;
+            tiles += n;
+            if (half * kHalf >= rows) continue;
+            const int32_t* trow = c.table + (int64_t)g.b * c.max_pages;
+            // row `col` of the block: node i of the lane, head `head`
+            const int i = blk * p.per_block + col / G, head = g.h * G + col % G;
+            uint64_t vis = 0;
+            if (col < rows) {
+                vis = a.mask ? a.mask[lo + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
+                if (nodes < 64) vis &= (1ull << nodes) - 1;
+            }
+            int pg[4];
+            auto pages_of = [&](int t) {
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const int slot = (g.t0 + t) * kTile + 32 * z + lane;
+                    pg[z] = slot < end ? trow[slot >> shift] : -1;
+                }
+            };
+            pages_of(0);
+            float neg_m = 0.f, l = 0.f;
+            for (int t = 0; t < n; ++t) {
+                const int slot0 = (g.t0 + t) * kTile;
+                uint32_t seen[4];
+                bool plain = slot0 + kTile <= len;
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    // an entry behind the last slot is -1
+                    seen[z] = __ballot_sync(0xffffffffu, pg[z] >= 0 && pg[z] < c.pages);
+                    plain = plain && seen[z] == 0xffffffffu;
+                }
+                if (!plain) {
+#pragma unroll
+                    for (int z = 0; z < 4; ++z) {
+                        const int ahead = len - (slot0 + 32 * z);  // context slots from here on
+                        const uint32_t context = ahead >= 32 ? 0xffffffffu : ahead > 0 ? (1u << ahead) - 1 : 0u;
+                        const uint32_t drafts = ahead >= 32    ? 0u
+                                                : ahead >= 0   ? (uint32_t)(vis << ahead)
+                                                : ahead > -64 ? (uint32_t)(vis >> -ahead)
+                                                              : 0u;
+                        seen[z] &= context | drafts;
+                    }
+                }
+                if (t + 1 < n) pages_of(t + 1);
+                ok = waitw(smem_addr(&s.sfull[half]), (did + t) & 1, abort);
+                if (!ok) break;
+                fence_after();
+                if (t == 0) neg_m = -fmaxf(row_top(at_s, sl, plain, seen), kUnseen);
+                uint32_t w[kTile / 2];
+                float sum;
+                const float over = weigh_row(at_s, sl, neg_m, plain, seen, w, sum);
+                if (__any_sync(0xffffffffu, over > kHeadroom)) {
+                    // Higher references.  The products of the tiles before are done: S waited for them.
+                    const float was = -neg_m, top = row_top(at_s, sl, plain, seen);
+                    const float now = over > kHeadroom ? fmaxf(top, was) : was;
+                    const float down = was == now ? 1.f : fast_exp2(was - now);
+                    l *= down;
+                    neg_m = -now;
+                    if (t > 0) {
+#pragma unroll 1
+                        for (int d = 0; d < D; d += 8) {
+                            float o[8];
+                            tm_ld(at_o + d, o);
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) o[j] *= down;
+                            tm_st8(at_o + d, o);
+                        }
+                    }
+                    weigh_row(at_s, sl, neg_m, plain, seen, w, sum);
+                }
+                l += sum;
+#pragma unroll
+                for (int z = 0; z < kTile / 2; z += 16) tm_st16(at_s + z, w + z);
+                tm_wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(smem_addr(&s.pfull[half]));
+            }
+            ok = ok && waitw(smem_addr(&s.odone[half]), seg & 1, abort);
+            ok = ok && waitw(smem_addr(&s.cleaned[(tiles - 1) % kCleaned]), ((tiles - 1) / kCleaned) & 1, abort);
+            if (!ok) break;
+            fence_after();
+            const bool whole = g.t0 == 0 && g.t1 == s.lanes.tiles[g.b];
+            const int64_t part = ((int64_t)blockIdx.x * 2 + (g.first <= u0 ? 0 : 1)) * 256 + col;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
+            if (col < rows) {
+                if (!whole)
+                    p.part_ml[part] = make_float2(-neg_m, l);
+                else if (a.lse)
+                    a.lse[(lo + i) * a.q_heads + head] = l == 0.f ? -INFINITY : (log2f(l) - neg_m) * 0.6931471805599453f;
+            }
+            const uint64_t badv = s.bad_v & vis;
+            uint16_t* out = (uint16_t*)a.out + (int64_t)(lo + i) * a.ldo + (int64_t)head * D;
+            float* po = p.part_o + part * D;
+#pragma unroll 1
+            for (int d = 0; d < D; d += 8) {
+                float o[8];
+                tm_ld(at_o + d, o);
+                for (uint64_t b = badv; b; b &= b - 1) {
+                    const int slot = len + __ffsll(b) - 1;
+                    const __nv_bfloat16* v = (const __nv_bfloat16*)c.v +
+                                             ((((int64_t)a.layer * c.pages + trow[slot >> shift]) * c.kv_heads + g.h) *
+                                                  c.page_size + (slot & (c.page_size - 1))) * D + d;
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float x = __bfloat162float(v[j]);
+                        if (!isfinite(x)) o[j] += x;
+                    }
+                }
+                if (col < rows && whole) {
+                    uint32_t h[4];
+#pragma unroll
+                    for (int j = 0; j < 8; j += 2) {
+                        const __nv_bfloat162 y = __floats2bfloat162_rn(o[j] * inv, o[j + 1] * inv);
+                        h[j / 2] = *reinterpret_cast<const uint32_t*>(&y);
+                    }
+                    *reinterpret_cast<uint4*>(out + d) = make_uint4(h[0], h[1], h[2], h[3]);
+                } else if (col < rows) {
+                    *reinterpret_cast<float4*>(po + d) = make_float4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<float4*>(po + d + 4) = make_float4(o[4], o[5], o[6], o[7]);
+                }
+                __syncwarp();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_addr(&s.left[half]));
+            did += n;
+            ++seg;
+        }
+        if (!ok && lane == 0) give_up(abort);
     }
     fence_before();
     __syncthreads();
@@ -1168,11 +1637,11 @@ int query_map(EncodeFn encode, const nvfp4_attn_args& a, int g, int q_box, CUten
     return r == CUDA_SUCCESS ? NVFP4_OK : fail_cuda(cudaErrorInvalidValue);
 }
 
-// Query rows per block: what one lane is expected to have, at most 128.
-int block_rows(int max_nodes, int rows, int g)
+// Query rows per block: what one lane is expected to have.
+int block_rows(int max_nodes, int rows, int g, int head_dim)
 {
     const int r = (max_nodes < rows ? max_nodes : rows) * g;
-    return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : 128;
+    return r <= 16 ? 16 : r <= 32 ? 32 : r <= 64 ? 64 : r <= 128 || head_dim > 128 ? 128 : 256;
 }
 
 struct Workspace {
@@ -1181,10 +1650,20 @@ struct Workspace {
 Workspace workspace(int head_dim, int sms)
 {
     // two parts per CTA at the widest block
+    const int rows = block_rows(NVFP4_ATTN_MAX_ROWS, NVFP4_ATTN_MAX_ROWS, 32, head_dim);
     Workspace w;
-    w.o = (size_t)sms * 2 * 128 * sizeof(float2);
-    w.bytes = w.o + (size_t)sms * 2 * 128 * head_dim * sizeof(float);
+    w.o = (size_t)sms * 2 * rows * sizeof(float2);
+    w.bytes = w.o + (size_t)sms * 2 * rows * head_dim * sizeof(float);
     return w;
+}
+
+template <int D, int N>
+auto kernel_of()
+{
+    if constexpr (N == 256)
+        return attn_wide_kernel<D>;
+    else
+        return attn_kernel<D, N>;
 }
 
 template <int D, int N>
@@ -1198,11 +1677,12 @@ int launch_variant(const AttnParams& p, const CUtensorMap& mk, const CUtensorMap
     int dev = 0;
     NVFP4_CUDA_TRY(cudaGetDevice(&dev));
     if (dev >= 64) return NVFP4_ERR_ARG;
+    const auto kernel = kernel_of<D, N>();
     if (!(ready.load() >> dev & 1)) {
-        NVFP4_CUDA_TRY(cudaFuncSetAttribute(attn_kernel<D, N>, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
+        NVFP4_CUDA_TRY(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes));
         ready.fetch_or(1ull << dev);
     }
-    NVFP4_CUDA_TRY(launch_pdl(attn_kernel<D, N>, dim3((unsigned)p.ctas), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
+    NVFP4_CUDA_TRY(launch_pdl(kernel, dim3((unsigned)p.ctas), dim3(L::kThreads), kBytes, stream, p, mk, mv, mq));
     // where no pair can be cut, whatever the lengths, there is nothing to join
     const int lanes = p.c.lanes < p.a.rows ? p.c.lanes : p.a.rows;
     const int64_t tiles = ((int64_t)p.c.max_pages * p.c.page_size + kTile - 1) / kTile;
@@ -1222,8 +1702,10 @@ int launch_dim(int n, const AttnParams& p, const CUtensorMap& mk, const CUtensor
     case 16: return launch_variant<D, 16>(p, mk, mv, mq, stream);
     case 32: return launch_variant<D, 32>(p, mk, mv, mq, stream);
     case 64: return launch_variant<D, 64>(p, mk, mv, mq, stream);
-    default: return launch_variant<D, 128>(p, mk, mv, mq, stream);
+    case 128: return launch_variant<D, 128>(p, mk, mv, mq, stream);
     }
+    if constexpr (D <= 128) return launch_variant<D, 256>(p, mk, mv, mq, stream);
+    return NVFP4_ERR_SHAPE;  // not reached: blocks of 256 are for heads of up to 128
 }
 
 }  // namespace
@@ -1282,7 +1764,7 @@ int launch_attn(const nvfp4_attn_args* a, cudaStream_t stream)
     if (st == NVFP4_OK) st = page_map(encode, p.c, p.c.v, a->layer, &mv);
     if (st != NVFP4_OK) return st;
     // at least one whole row per block, so a lane has at most 64 blocks
-    const int g = a->q_heads / p.c.kv_heads, n = block_rows(a->max_nodes, a->rows, g);
+    const int g = a->q_heads / p.c.kv_heads, n = block_rows(a->max_nodes, a->rows, g, p.c.head_dim);
     p.per_block = n / g;
     p.q_box = p.per_block < a->rows ? p.per_block : a->rows;
     CUtensorMap mq;

@@ -314,3 +314,141 @@ def test_helper_refuses(dev):
         x = kw.pop("q")
         with pytest.raises(ValueError):
             abi.attn_tree(c, 0, x, 0.1, **kw)
+
+
+# ------------------- lanes of more than 128 query rows to a cached head (heads of 64 and 128)
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("n", [0, 1, 64, 127, 128, 192, 1000])
+def test_wide_trees_at_tile_borders(dev, n, dim):
+    """The drafted slots begin before, on and behind a tile's border and reach into a second one."""
+    check(dev, 40 + n, [n], [64], 8, 2, dim, 16)
+
+
+@pytest.mark.parametrize("counts,hq,hkv", [([33], 4, 1), ([64], 5, 1), ([43], 3, 1), ([5, 59], 32, 1), ([64], 32, 1),
+                                           ([1, 40, 0, 3, 20], 8, 2), ([2] * 6 + [50], 12, 2), ([9, 9], 15, 1)])
+def test_wide_heads_and_lanes(dev, counts, hq, hkv):
+    """A second half with a few rows, rows split between the halves, several blocks to a lane, narrow lanes between."""
+    lens = [int(x) for x in np.random.default_rng(hq).integers(0, 900, len(counts))]
+    check(dev, 41, lens, counts, hq, hkv, 128, 32)
+    check(dev, 42, lens, counts, hq, hkv, 64, 16, kind="chain")
+
+
+def test_wide_long_context(dev):
+    """Pairs cut between CTAs and joined."""
+    check(dev, 43, [9000, 20011], [40, 24], 8, 1, 128, 64)
+
+
+@pytest.mark.parametrize("scale,spread", [(8.0, 4.0), (0.0, 1.0), (-0.3, 1.0)])
+def test_wide_sharp_and_flat_scores(dev, scale, spread):
+    check(dev, 44, [900], [40], 8, 2, 128, 64, scale=scale, spread=spread)
+
+
+@pytest.mark.parametrize("scale", [0.25, -0.25, 40.0])
+def test_wide_running_maximum(dev, scale):
+    """Every tile has a new maximum, for every second row; the others' scores fall."""
+    rows = 36
+    c, r = ch.make(dev, 45, [700], [rows], hkv=1, page=16, dim=64)
+    for s in range(700 + rows):
+        p, o = r.where(0, s)
+        r.k[0, p, 0, o] = cache_ref.bf16_bits(np.full(64, s / 64.0))
+    c = ch.device_cache(dev, r.k, r.v, r.table, r.len, r.ref)
+    x = np.ones((rows, 4, 64))
+    x[1::2] = -1.0
+    q = ch.dev_bf16(cache_ref.bf16_bits(x), dev)
+    out, lse = abi.attn_tree(c, 0, q, scale, row_start=ch.ints([0, rows], dev), max_nodes=rows, want_lse=True)
+    torch.cuda.synchronize()
+    compare(c, r, q, scale, [0, rows], None, out, lse)
+
+
+def test_wide_rows_that_see_nothing(dev):
+    rows = 48
+    c, r = ch.make(dev, 46, [0, 20], [40, 8], hkv=1, dim=128)
+    q = torch.randn((rows, 8, 128), device=dev).to(torch.bfloat16)
+    mask = [0 if i % 3 == 0 else 1 << i | 1 for i in range(40)] + [0] * 8
+    start = [0, 40, 48]
+    out, lse = abi.attn_tree(c, 0, q, 0.1, row_start=ch.ints(start, dev), mask=ch.words(mask, dev), max_nodes=40,
+                             want_lse=True)
+    torch.cuda.synchronize()
+    got, gl = compare(c, r, q, 0.1, start, mask, out, lse)
+    assert not got[0:40:3].any() and np.isneginf(gl[0:40:3]).all()
+
+
+@pytest.mark.parametrize("dim", [64, 128])
+@pytest.mark.parametrize("value", SPECIAL)
+def test_wide_unseen_slots_never_reach_a_row(dev, value, dim):
+    lens, counts = [100, 37], [40, 24]
+    c, r = ch.make(dev, 47, lens, counts, hkv=2, page=16, dim=dim)
+    start = [0, 40, 64]
+    mask = [1 << i | 1 for i in range(40)] + [1 << i | 1 for i in range(24)]
+    q = torch.randn((64, 16, dim), device=dev).to(torch.bfloat16)
+    kw = dict(row_start=ch.ints(start, dev), mask=ch.words(mask, dev), max_nodes=40, want_lse=True)
+    clean, clean_lse = abi.attn_tree(c, 0, q, 0.1, **kw)
+    bad = cache_ref.bf16_bits(np.full(dim, value))
+    touched = set()
+    for b in range(2):
+        for j in (3, 11, 20):  # seen by the rows j alone
+            p, o = r.where(b, lens[b] + j)
+            r.v[0, p, :, o], r.k[0, p, :, o] = bad, bad
+            touched.add(start[b] + j)
+        last = lens[b] + counts[b]
+        for s in range(last, -(-last // 16) * 16):
+            p, o = r.where(b, s)
+            r.v[0, p, :, o], r.k[0, p, :, o] = bad, bad
+    free = r.ref == 0
+    r.k[0, free], r.v[0, free] = bad, bad
+    c2 = ch.device_cache(dev, r.k, r.v, r.table, r.len, r.ref)
+    out, lse = abi.attn_tree(c2, 0, q, 0.1, **kw)
+    torch.cuda.synchronize()
+    rest = [i for i in range(64) if i not in touched]
+    assert torch.equal(out[rest], clean[rest]) and torch.equal(lse[rest], clean_lse[rest])
+    if not np.isfinite(value):
+        assert not torch.isfinite(out[sorted(touched)].float()).all(-1).any()
+
+
+@pytest.mark.parametrize("value", [np.nan, np.inf, -np.inf])
+def test_wide_value_that_is_seen_shows(dev, value):
+    c, r = ch.make(dev, 48, [120], [40], hkv=1, page=16, dim=128)
+    for node, d in ((2, 5), (30, 100)):
+        p, o = r.where(0, 120 + node)
+        r.v[0, p, 0, o, d] = cache_ref.bf16_bits(np.array([value]))[0]
+    c2 = ch.device_cache(dev, r.k, r.v, r.table, r.len, r.ref)
+    q = torch.randn((40, 4, 128), device=dev).to(torch.bfloat16)
+    mask = [1 << i | (1 << 2 if i in (7, 33) else 0) | (1 << 30 if i in (31, 33) else 0) for i in range(40)]
+    out, lse = abi.attn_tree(c2, 0, q, 0.1, row_start=ch.ints([0, 40], dev), mask=ch.words(mask, dev), max_nodes=40,
+                             want_lse=True)
+    torch.cuda.synchronize()
+    compare(c2, r, q, 0.1, [0, 40], mask, out, lse)
+    bad = ~torch.isfinite(out.float())
+    assert bad[[2, 7, 33], :, 5].all() and bad[[30, 31, 33], :, 100].all() and int(bad.sum()) == 24
+
+
+def test_wide_bad_pages_are_not_seen(dev):
+    c, r = ch.make(dev, 49, [300, 60], [40, 1], hkv=1, page=16, dim=128)
+    for b, col, e in ((0, 2, 1 << 24), (0, 9, -1), (0, 20, 1 << 20), (1, 0, -7)):
+        c.table[b, col] = e
+        r.table[b, col] = e
+    q = torch.randn((41, 4, 128), device=dev).to(torch.bfloat16)
+    out, lse = abi.attn_tree(c, 0, q, 0.1, row_start=ch.ints([0, 40, 41], dev), max_nodes=40, want_lse=True)
+    torch.cuda.synchronize()
+    compare(c, r, q, 0.1, [0, 40, 41], None, out, lse)
+    assert ch.clean_status() == 128
+
+
+def test_wide_same_from_call_to_call_and_in_a_graph(dev):
+    c, r = ch.make(dev, 50, [3000, 500], [40, 24], hkv=2, page=32, dim=128)
+    q = torch.randn((64, 16, 128), device=dev).to(torch.bfloat16)
+    ws = abi.attn_tree_workspace(c, 64, 16)
+    kw = dict(row_start=ch.ints([0, 40, 64], dev), max_nodes=40, workspace=ws)
+    first = abi.attn_tree(c, 0, q, 0.1, **kw)
+    abi.attn_tree(c, 0, q[:2], 0.1, workspace=ws)
+    out = torch.zeros_like(first)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        abi.attn_tree(c, 0, q, 0.1, out=out, **kw)
+    for _ in range(10):
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, first)
+        out.zero_()
