@@ -1103,33 +1103,16 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
 
 // ---------------------------------------------------- many rows to a head
 
-// 128 log2 scores of a row, 32 at a time with the next ones on their way: f(i,
-// x) gets those from slot i on, x = s scale log2(e) + neg_m, masked ones -inf.
-// `plain`: every slot is seen.
-template <class F>
-__device__ __forceinline__ void row_scores(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[4], F f)
+// 32 of a row's scores as log2 weights, x = s scale log2(e) + neg_m; those not in `seen` -inf.
+__device__ __forceinline__ void log2_weights(float (&x)[32], float sl, float neg_m, bool plain, uint32_t seen)
 {
     const f32x2 scale = pair(sl, sl), minus = pair(neg_m, neg_m);
-    float x[2][32];
-    tm_ld16(at, x[0]);
-    tm_ld16(at + 16, x[0] + 16);
 #pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        float(&y)[32] = x[c & 1];
-        tm_wait_ld();
-        settled(y);
-        if (c < 3) {
-            tm_ld16(at + 32 * (c + 1), x[(c + 1) & 1]);
-            tm_ld16(at + 32 * (c + 1) + 16, x[(c + 1) & 1] + 16);
-        }
+    for (int i = 0; i < 32; i += 2) unpair(fma2(pair(x[i], x[i + 1]), scale, minus), x[i], x[i + 1]);
+    if (!plain) {
 #pragma unroll
-        for (int i = 0; i < 32; i += 2) unpair(fma2(pair(y[i], y[i + 1]), scale, minus), y[i], y[i + 1]);
-        if (!plain) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-                if (!(seen[c] >> i & 1)) y[i] = -INFINITY;
-        }
-        f(32 * c, y);
+        for (int i = 0; i < 32; ++i)
+            if (!(seen >> i & 1)) x[i] = -INFINITY;
     }
 }
 
@@ -1137,10 +1120,14 @@ __device__ __forceinline__ void row_scores(uint32_t at, float sl, float neg_m, b
 __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, const uint32_t (&seen)[4])
 {
     float top = -INFINITY;
-    row_scores(at, sl, 0.f, plain, seen, [&](int, const float (&x)[32]) {
+#pragma unroll 1
+    for (int c = 0; c < 4; ++c) {
+        float x[32];
+        tm_ld(at + 32 * c, x);
+        log2_weights(x, sl, 0.f, plain, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
-    });
+    }
     return top;
 }
 
@@ -1149,13 +1136,25 @@ __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, cons
 __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[4],
                                            uint32_t (&w)[kTile / 2], float& sum)
 {
-    float over = -INFINITY;
+    float over = -INFINITY, over2 = -INFINITY;
     f32x2 s0 = 0, s1 = 0;
-    row_scores(at, sl, neg_m, plain, seen, [&](int i0, float (&x)[32]) {
+    float buf[2][32];
+    tm_ld16(at, buf[0]);
+    tm_ld16(at + 16, buf[0] + 16);
+#pragma unroll
+    for (int z = 0; z < 4; ++z) {  // 32 at a time, the next ones on their way
+        float(&x)[32] = buf[z & 1];
+        tm_wait_ld();
+        settled(x);
+        if (z < 3) {
+            tm_ld16(at + 32 * (z + 1), buf[(z + 1) & 1]);
+            tm_ld16(at + 32 * (z + 1) + 16, buf[(z + 1) & 1] + 16);
+        }
+        log2_weights(x, sl, neg_m, plain, seen[z]);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
             over = max3(over, x[i], x[i + 1]);
-            over = max3(over, x[i + 2], x[i + 3]);
+            over2 = max3(over2, x[i + 2], x[i + 3]);
 #pragma unroll
             for (int j = i; j < i + 4; ++j) x[j] = fast_exp2(x[j]);
             s0 = add2(s0, pair(x[i], x[i + 1]));
@@ -1163,15 +1162,15 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
 #pragma unroll
             for (int j = i; j < i + 4; j += 2) {
                 const __nv_bfloat162 h = __floats2bfloat162_rn(x[j], x[j + 1]);
-                w[(i0 + j) / 2] = *reinterpret_cast<const uint32_t*>(&h);
+                w[16 * z + j / 2] = *reinterpret_cast<const uint32_t*>(&h);
             }
         }
-    });
+    }
     float a, b, c, d;
     unpair(s0, a, b);
     unpair(s1, c, d);
     sum = (a + b) + (c + d);
-    return over;
+    return fmaxf(over, over2);
 }
 
 // For lanes with more than 128 query rows to a cached head.  The rows are the
@@ -1408,28 +1407,33 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                 ok = waitw(smem_addr(&s.sfull[half]), (did + t) & 1, abort);
                 if (!ok) break;
                 fence_after();
-                if (t == 0) neg_m = -fmaxf(row_top(at_s, sl, plain, seen), kUnseen);
                 uint32_t w[kTile / 2];
                 float sum;
-                const float over = weigh_row(at_s, sl, neg_m, plain, seen, w, sum);
-                if (__any_sync(0xffffffffu, over > kHeadroom)) {
-                    // Higher references.  The products of the tiles before are done: S waited for them.
-                    const float was = -neg_m, top = row_top(at_s, sl, plain, seen);
-                    const float now = over > kHeadroom ? fmaxf(top, was) : was;
-                    const float down = was == now ? 1.f : fast_exp2(was - now);
-                    l *= down;
-                    neg_m = -now;
-                    if (t > 0) {
+                // The first tile's largest scores are the references; later ones rise where
+                // a score passes them by more than the headroom (seen when the weights are formed).
+                bool rise = t == 0;
 #pragma unroll 1
-                        for (int d = 0; d < D; d += 8) {
-                            float o[8];
-                            tm_ld(at_o + d, o);
+                for (int turn = 0; turn < 2; ++turn) {
+                    if (__any_sync(0xffffffffu, rise)) {
+                        // (the products of the tiles before are done: S waited for them)
+                        const float was = t == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
+                        const float now = rise ? fmaxf(top, was) : was;
+                        const float down = was == now ? 1.f : fast_exp2(was - now);
+                        l *= down;
+                        neg_m = -now;
+                        if (t > 0) {
+#pragma unroll 1
+                            for (int d = 0; d < D; d += 8) {
+                                float o[8];
+                                tm_ld(at_o + d, o);
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) o[j] *= down;
-                            tm_st8(at_o + d, o);
+                                for (int j = 0; j < 8; ++j) o[j] *= down;
+                                tm_st8(at_o + d, o);
+                            }
                         }
                     }
-                    weigh_row(at_s, sl, neg_m, plain, seen, w, sum);
+                    rise = weigh_row(at_s, sl, neg_m, plain, seen, w, sum) > kHeadroom;
+                    if (!__any_sync(0xffffffffu, rise)) break;
                 }
                 l += sum;
 #pragma unroll
