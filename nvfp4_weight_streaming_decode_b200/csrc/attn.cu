@@ -124,7 +124,7 @@ constexpr int kCleaned = 8;  // more than the tiles of V a ring holds
 
 struct Shared {  // at kOffMisc
     uint64_t full[12], empty[12];
-    uint64_t sfull[2], pfull[2], pfree[2];
+    uint64_t sfull[4], pfull[4], pfree[2];
     uint64_t qfull, qempty, ofull, drain;
     uint64_t cleaned[kCleaned], odone[2], left[2];  // of attn_wide_kernel
     uint32_t tmem;
@@ -684,9 +684,11 @@ __device__ __forceinline__ void start_cta(const AttnParams& p, Shared& s, uint8_
             mbar_init(smem_addr(&s.full[i]), 1);
             mbar_init(smem_addr(&s.empty[i]), 1);
         }
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < (L::kWide ? 4 : 2); ++i) {
             mbar_init(smem_addr(&s.sfull[i]), 1);
             mbar_init(smem_addr(&s.pfull[i]), L::kWide ? 4 : L::kSoftWarps);
+        }
+        for (int i = 0; i < 2; ++i) {
             mbar_init(smem_addr(&s.pfree[i]), 1);
         }
         mbar_init(smem_addr(&s.qfull), 1);
@@ -1116,15 +1118,15 @@ __device__ __forceinline__ void log2_weights(float (&x)[32], float sl, float neg
     }
 }
 
-// The largest of a row's 128 log2 scores.
-__device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, const uint32_t (&seen)[4])
+// The largest of a row's 64 log2 scores.
+__device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, const uint32_t (&seen)[2])
 {
     float top = -INFINITY;
 #pragma unroll 1
-    for (int c = 0; c < 4; ++c) {
+    for (int c = 0; c < 2; ++c) {
         float x[32];
         tm_ld(at + 32 * c, x);
-        log2_weights(x, sl, 0.f, plain, c == 0 ? seen[0] : c == 1 ? seen[1] : c == 2 ? seen[2] : seen[3]);
+        log2_weights(x, sl, 0.f, plain, c == 0 ? seen[0] : seen[1]);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
     }
@@ -1133,8 +1135,8 @@ __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, cons
 
 // A row's weights as packed bf16 pairs, and their sum (of the weights before
 // their rounding); returns the largest log2 weight.
-__device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[4],
-                                           uint32_t (&w)[kTile / 2], float& sum)
+__device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[2],
+                                           uint32_t (&w)[32], float& sum)
 {
     float over = -INFINITY, over2 = -INFINITY;
     f32x2 s0 = 0, s1 = 0;
@@ -1142,13 +1144,13 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
     tm_ld16(at, buf[0]);
     tm_ld16(at + 16, buf[0] + 16);
 #pragma unroll
-    for (int z = 0; z < 4; ++z) {  // 32 at a time, the next ones on their way
-        float(&x)[32] = buf[z & 1];
+    for (int z = 0; z < 2; ++z) {  // 32 at a time, the next ones on their way
+        float(&x)[32] = buf[z];
         tm_wait_ld();
         settled(x);
-        if (z < 3) {
-            tm_ld16(at + 32 * (z + 1), buf[(z + 1) & 1]);
-            tm_ld16(at + 32 * (z + 1) + 16, buf[(z + 1) & 1] + 16);
+        if (z == 0) {
+            tm_ld16(at + 32, buf[1]);
+            tm_ld16(at + 48, buf[1] + 16);
         }
         log2_weights(x, sl, neg_m, plain, seen[z]);
 #pragma unroll
@@ -1178,17 +1180,17 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
 //     S [128 rows][128 slots] = Q K^T,   O [128 rows][D] += P V
 // so a thread owns a row: no maximum or sum crosses threads, and P goes back to
 // tensor memory, over the scores it came from, which takes its 32 KB (written
-// and read) out of the shared memory's way.  A CTA has two halves of 128 rows, four warps
-// each, that take turns: while one half's warps form weights, the tensor cores
-// work for the other.  V is shared, so one more warp looks after its slots that
-// rows must not see, ahead of the products.
+// and read) out of the shared memory's way.  A CTA has two halves of 128 rows,
+// four warps each.  Scores come in steps of 64 slots and two buffers, so that a half's warps
+// have the next scores while the tensor cores take up the weights of the last.
+// V is shared, so one more warp looks after its slots that rows must not see, ahead of the products.
 template <int D>
 __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
     attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
                      const __grid_constant__ CUtensorMap map_v, const __grid_constant__ CUtensorMap map_q)
 {
     using L = Plan<D, 256>;
-    constexpr int kHalf = 128, kSoftWarps = L::kSoftWarps, kLoadWarp = L::kLoadWarp, kMmaWarp = L::kMmaWarp,
+    constexpr int kHalf = 128, kStep = kTile / 2, kSoftWarps = L::kSoftWarps, kLoadWarp = L::kLoadWarp, kMmaWarp = L::kMmaWarp,
                   kQWarp = L::kMmaWarp + 1;
     extern __shared__ uint8_t raw[];
     uint8_t* sm = raw + ((1024 - (smem_addr(raw) & 1023)) & 1023);
@@ -1204,7 +1206,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
 
     start_cta<L>(p, s, sm, map_k, map_v, map_q);
     const uint32_t tmem = s.tmem;
-    const uint32_t tm_s = tmem, tm_o = tmem + 2 * kTile;  // [half][128 columns] each
+    const uint32_t tm_s = tmem, tm_o = tmem + 4 * kStep;  // [half][2 steps][64], [half][128]
     const int units = s.lanes.base[kMaxLanes], width = s.lanes.width, groups = s.lanes.groups;
     const int group = blockIdx.x / width, blk = blockIdx.x % width;
     const bool idle = group >= groups;
@@ -1219,68 +1221,75 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
         // ---- the products
         const uint32_t lead = elect();
         constexpr uint32_t kBase = (1u << 4) | (1u << 7) | (1u << 10) | (8u << 24);
-        constexpr uint32_t kIdS = kBase | ((uint32_t)(kTile >> 3) << 17);
+        constexpr uint32_t kIdS = kBase | ((uint32_t)(kStep >> 3) << 17);
         constexpr uint32_t kIdO = kBase | (1u << 16) | ((uint32_t)(D >> 3) << 17);
         int idx = 0, seg = 0, tiles = 0;
-        int did[2] = {0, 0};  // tiles of earlier segments, per half
+        int did[2] = {0, 0};     // steps of earlier segments, per half
+        int issued[2] = {0, 0};  // products P V, per half
         bool ok = true;
         for (int u = u0; ok && u < u1;) {
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u = g.next;
             if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
-            const int n = g.t1 - g.t0;
+            const int n = g.t1 - g.t0, steps = 2 * n;
             const int halves = min(p.per_block, s.lanes.nodes[g.b] - blk * p.per_block) * G > kHalf ? 2 : 1;
             ok = waitw(smem_addr(&s.qfull), seg & 1, abort);
-            // S of a tile, over the weights of the tile before
-            auto scores = [&](int t, int w) {
-                const int q = idx + pos_k(t), slot = q % L::kRing, T = did[w] + t;
-                if (w == 0 && !waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort)) return false;
-                if (T > 0 && !waitw(smem_addr(&s.pfree[w]), (T - 1) & 1, abort)) return false;
+            // S of step i (half a tile), where the weights of the step before the last were
+            auto scores = [&](int i, int w) {
+                if (i >= steps) return true;
+                const int t = i / 2, q = idx + pos_k(t), slot = q % L::kRing, S = did[w] + i;
+                if (w == 0 && i % 2 == 0 && !waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort)) return false;
+                if (issued[w] > 0 && !waitw(smem_addr(&s.pfree[w]), (issued[w] - 1) & 1, abort)) return false;
                 fence_after();
+                const uint32_t at = tm_s + (2 * w + S % 2) * kStep, rows = i % 2 * kStep * 128;
 #pragma unroll
                 for (int x = 0; x < L::kAtoms; ++x)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        mma(lead, tm_s + w * kTile, desc_k(qbuf + x * 256 * 128 + w * kHalf * 128 + k * 32),
-                            desc_k(ring + slot * L::kEntry + x * kTile * 128 + k * 32), kIdS, (x | k) != 0);
-                commit(lead, smem_addr(&s.sfull[w]));
-                if (w == halves - 1) {
+                        mma(lead, at, desc_k(qbuf + x * 256 * 128 + w * kHalf * 128 + k * 32),
+                            desc_k(ring + slot * L::kEntry + x * kTile * 128 + rows + k * 32), kIdS, (x | k) != 0);
+                commit(lead, smem_addr(&s.sfull[2 * w + S % 2]));
+                if (w == halves - 1 && i % 2) {
                     commit(lead, smem_addr(&s.empty[slot]));
-                    if (t == n - 1) commit(lead, smem_addr(&s.qempty));
+                    if (i == steps - 1) commit(lead, smem_addr(&s.qempty));
                 }
                 return true;
             };
+            // O of step i
+            auto values = [&](int i, int w) {
+                const int t = i / 2, q = idx + pos_v(t, n), slot = q % L::kRing, S = did[w] + i, V = tiles + t;
+                if (w == 0 && i % 2 == 0 &&
+                    (!waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort) ||
+                     !waitw(smem_addr(&s.cleaned[V % kCleaned]), (V / kCleaned) & 1, abort)))
+                    return false;
+                if (!waitw(smem_addr(&s.pfull[2 * w + S % 2]), (S / 2) & 1, abort)) return false;
+                fence_after();
+                const uint32_t at = tm_s + (2 * w + S % 2) * kStep;
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                if (w < halves) ok = ok && scores(0, w);
-            for (int t = 0; ok && t < n; ++t) {
-                const int q = idx + pos_v(t, n), slot = q % L::kRing, V = tiles + t;
-#pragma unroll
-                for (int w = 0; w < 2; ++w) {
-                    if (w >= halves || !ok) continue;
-                    if (w == 0)
-                        ok = waitw(smem_addr(&s.full[slot]), (q / L::kRing) & 1, abort) &&
-                             waitw(smem_addr(&s.cleaned[V % kCleaned]), (V / kCleaned) & 1, abort);
-                    ok = ok && waitw(smem_addr(&s.pfull[w]), (did[w] + t) & 1, abort);
-                    if (!ok) continue;
-                    fence_after();
-#pragma unroll
-                    for (int k = 0; k < kTile / 16; ++k)
-                        mma_tm(lead, tm_o + w * kHalf, tm_s + w * kTile + 8 * k,
-                               desc_mn(ring + slot * L::kEntry + k * 2048, L::kAtoms == 2 ? kTile * 128 : 0), kIdO,
-                               t > 0 || k != 0);
-                    commit(lead, smem_addr(&s.pfree[w]));
-                    if (w == halves - 1) commit(lead, smem_addr(&s.empty[slot]));
-                    if (t == n - 1)
-                        commit(lead, smem_addr(&s.odone[w]));
-                    else
-                        ok = scores(t + 1, w);
-                }
+                for (int k = 0; k < kStep / 16; ++k)
+                    mma_tm(lead, tm_o + w * kHalf, at + 8 * k,
+                           desc_mn(ring + slot * L::kEntry + (i % 2 * (kStep / 16) + k) * 2048,
+                                   L::kAtoms == 2 ? kTile * 128 : 0),
+                           kIdO, i > 0 || k != 0);
+                commit(lead, smem_addr(&s.pfree[w]));
+                ++issued[w];
+                if (w == halves - 1 && i % 2) commit(lead, smem_addr(&s.empty[slot]));
+                if (i == steps - 1) commit(lead, smem_addr(&s.odone[w]));
+                return true;
+            };
+            if (halves == 2) {
+                // each half's scores follow the other half's values, when its own last values are done
+                ok = ok && scores(0, 0) && scores(0, 1) && scores(1, 0);
+                for (int i = 0; ok && i < steps; ++i)
+                    ok = values(i, 0) && scores(i + 1, 1) && values(i, 1) && scores(i + 2, 0);
+            } else {
+                ok = ok && scores(0, 0) && scores(1, 0);
+                for (int i = 0; ok && i < steps; ++i) ok = values(i, 0) && scores(i + 2, 0);
             }
             idx += 2 * n;
             tiles += n;
-            did[0] += n;
-            if (halves == 2) did[1] += n;
+            did[0] += steps;
+            if (halves == 2) did[1] += steps;
             ++seg;
         }
         if (!ok && lane == 0) give_up(abort);
@@ -1350,7 +1359,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
         // ---- softmax: thread = row
         const int half = warp >> 2, quad = warp & 3, col = half * kHalf + quad * 32 + lane;
         const uint32_t lanebits = (uint32_t)(quad * 32) << 16;
-        const uint32_t at_s = tm_s + half * kTile + lanebits, at_o = tm_o + half * kHalf + lanebits;
+        const uint32_t at_half = tm_s + 2 * half * kStep + lanebits, at_o = tm_o + half * kHalf + lanebits;
         const float sl = a.scale * 1.4426950408889634f;
         int seg = 0, did = 0, tiles = 0;
         bool ok = true;
@@ -1358,7 +1367,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
             const Segment g = segment_at(s.lanes, c.lanes, u, u1);
             u = g.next;
             if (g.t1 <= g.t0 || blk * p.per_block >= s.lanes.nodes[g.b]) continue;
-            const int n = g.t1 - g.t0;
+            const int n = g.t1 - g.t0, steps = 2 * n;
             const int len = s.lanes.len[g.b], end = s.lanes.end[g.b], lo = s.lanes.lo[g.b], nodes = s.lanes.nodes[g.b];
             const int rows = min(p.per_block, nodes - blk * p.per_block) * G;
             tiles += n;
@@ -1371,29 +1380,30 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                 vis = a.mask ? a.mask[lo + i] : (i >= 63 ? ~0ull : (2ull << i) - 1);
                 if (nodes < 64) vis &= (1ull << nodes) - 1;
             }
-            int pg[4];
-            auto pages_of = [&](int t) {
+            int pg[2];
+            auto pages_of = [&](int i) {
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const int slot = (g.t0 + t) * kTile + 32 * z + lane;
+                for (int z = 0; z < 2; ++z) {
+                    const int slot = g.t0 * kTile + i * kStep + 32 * z + lane;
                     pg[z] = slot < end ? trow[slot >> shift] : -1;
                 }
             };
             pages_of(0);
             float neg_m = 0.f, l = 0.f;
-            for (int t = 0; t < n; ++t) {
-                const int slot0 = (g.t0 + t) * kTile;
-                uint32_t seen[4];
-                bool plain = slot0 + kTile <= len;
+            for (int st = 0; st < steps; ++st) {
+                const int slot0 = g.t0 * kTile + st * kStep, S = did + st;
+                const uint32_t at_s = at_half + S % 2 * kStep;
+                uint32_t seen[2];
+                bool plain = slot0 + kStep <= len;
 #pragma unroll
-                for (int z = 0; z < 4; ++z) {
+                for (int z = 0; z < 2; ++z) {
                     // an entry behind the last slot is -1
                     seen[z] = __ballot_sync(0xffffffffu, pg[z] >= 0 && pg[z] < c.pages);
                     plain = plain && seen[z] == 0xffffffffu;
                 }
                 if (!plain) {
 #pragma unroll
-                    for (int z = 0; z < 4; ++z) {
+                    for (int z = 0; z < 2; ++z) {
                         const int ahead = len - (slot0 + 32 * z);  // context slots from here on
                         const uint32_t context = ahead >= 32 ? 0xffffffffu : ahead > 0 ? (1u << ahead) - 1 : 0u;
                         const uint32_t drafts = ahead >= 32    ? 0u
@@ -1403,25 +1413,27 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                         seen[z] &= context | drafts;
                     }
                 }
-                if (t + 1 < n) pages_of(t + 1);
-                ok = waitw(smem_addr(&s.sfull[half]), (did + t) & 1, abort);
+                if (st + 1 < steps) pages_of(st + 1);
+                ok = waitw(smem_addr(&s.sfull[2 * half + S % 2]), (S / 2) & 1, abort);
                 if (!ok) break;
                 fence_after();
-                uint32_t w[kTile / 2];
+                uint32_t w[kStep / 2];
                 float sum;
-                // The first tile's largest scores are the references; later ones rise where
+                // The first step's largest scores are the references; later ones rise where
                 // a score passes them by more than the headroom (seen when the weights are formed).
-                bool rise = t == 0;
+                bool rise = st == 0;
 #pragma unroll 1
                 for (int turn = 0; turn < 2; ++turn) {
                     if (__any_sync(0xffffffffu, rise)) {
-                        // (the products of the tiles before are done: S waited for them)
-                        const float was = t == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
+                        const float was = st == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
                         const float now = rise ? fmaxf(top, was) : was;
                         const float down = was == now ? 1.f : fast_exp2(was - now);
                         l *= down;
                         neg_m = -now;
-                        if (t > 0) {
+                        if (st > 0) {
+                            // O so far, once the step before is in (S waited for the one before that)
+                            ok = ok && waitw(smem_addr(&s.pfree[half]), (S - 1) & 1, abort);
+                            fence_after();
 #pragma unroll 1
                             for (int d = 0; d < D; d += 8) {
                                 float o[8];
@@ -1435,13 +1447,14 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                     rise = weigh_row(at_s, sl, neg_m, plain, seen, w, sum) > kHeadroom;
                     if (!__any_sync(0xffffffffu, rise)) break;
                 }
+                if (!ok) break;
                 l += sum;
 #pragma unroll
-                for (int z = 0; z < kTile / 2; z += 16) tm_st16(at_s + z, w + z);
+                for (int z = 0; z < kStep / 2; z += 16) tm_st16(at_s + z, w + z);
                 tm_wait_st();
                 fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(smem_addr(&s.pfull[half]));
+                if (lane == 0) mbar_arrive(smem_addr(&s.pfull[2 * half + S % 2]));
             }
             ok = ok && waitw(smem_addr(&s.odone[half]), seg & 1, abort);
             ok = ok && waitw(smem_addr(&s.cleaned[(tiles - 1) % kCleaned]), ((tiles - 1) / kCleaned) & 1, abort);
@@ -1491,7 +1504,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
             fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(smem_addr(&s.left[half]));
-            did += n;
+            did += steps;
             ++seg;
         }
         if (!ok && lane == 0) give_up(abort);
