@@ -73,6 +73,7 @@ constexpr unsigned kBadPage = 1u, kGaveUp = 4u;
 constexpr int kTile = 128;                 // slots per tile
 constexpr int kMaxLanes = NVFP4_CACHE_MAX_LANES;
 constexpr float kHeadroom = 32.f;          // weights up to 2^32 before a rescale; their sums stay far below 2^127
+constexpr float kMostWeight = 4294967296.f;  // 2^kHeadroom
 constexpr float kUnseen = -3.0e38f;        // reference of a column that has seen no slot
 constexpr uint32_t kSleepNs = 1000;
 constexpr uint32_t kPolls = 1u << 20;      // about a second
@@ -97,7 +98,7 @@ struct Plan {
     static constexpr int kOffQ = kOffP + kPBufs * kPBytes;
     static constexpr int kOffMisc = kOffQ + kQBytes;
     // Softmax warps come in two groups of four (32 slots each), half the columns each.
-    static constexpr int kCols = kWide ? kTile : N / 2;      // columns per softmax thread
+    static constexpr int kCols = N / 2;                      // columns per softmax thread
     static constexpr int kSoftWarps = 8, kSoftThreads = 32 * kSoftWarps;
     static constexpr int kLoadWarp = kSoftWarps, kMmaWarp = kSoftWarps + 1;
     static constexpr int kThreads = kSoftThreads + 128;      // the last group: pages, products, queries, an idle warp
@@ -1133,12 +1134,10 @@ __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, cons
     return top;
 }
 
-// A row's weights as packed bf16 pairs, and their sum (of the weights before
-// their rounding); returns the largest log2 weight.
+// A row's weights as packed bf16 pairs; returns their sum (before the rounding).
 __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[2],
-                                           uint32_t (&w)[32], float& sum)
+                                           uint32_t (&w)[32])
 {
-    float over = -INFINITY, over2 = -INFINITY;
     f32x2 s0 = 0, s1 = 0;
     float buf[2][32];
     tm_ld16(at, buf[0]);
@@ -1155,8 +1154,6 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
         log2_weights(x, sl, neg_m, plain, seen[z]);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
-            over = max3(over, x[i], x[i + 1]);
-            over2 = max3(over2, x[i + 2], x[i + 3]);
 #pragma unroll
             for (int j = i; j < i + 4; ++j) x[j] = fast_exp2(x[j]);
             s0 = add2(s0, pair(x[i], x[i + 1]));
@@ -1171,8 +1168,7 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
     float a, b, c, d;
     unpair(s0, a, b);
     unpair(s1, c, d);
-    sum = (a + b) + (c + d);
-    return fmaxf(over, over2);
+    return (a + b) + (c + d);
 }
 
 // For lanes with more than 128 query rows to a cached head.  The rows are the
@@ -1419,8 +1415,9 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                 fence_after();
                 uint32_t w[kStep / 2];
                 float sum;
-                // The first step's largest scores are the references; later ones rise where
-                // a score passes them by more than the headroom (seen when the weights are formed).
+                // The first step's largest scores are the references; later ones rise where a
+                // score passes them by more than the headroom: then the weights' sum is above
+                // 2^kHeadroom, which costs nothing to see.
                 bool rise = st == 0;
 #pragma unroll 1
                 for (int turn = 0; turn < 2; ++turn) {
@@ -1444,7 +1441,8 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                             }
                         }
                     }
-                    rise = weigh_row(at_s, sl, neg_m, plain, seen, w, sum) > kHeadroom;
+                    sum = weigh_row(at_s, sl, neg_m, plain, seen, w);
+                    rise = sum > kMostWeight;
                     if (!__any_sync(0xffffffffu, rise)) break;
                 }
                 if (!ok) break;
