@@ -1471,8 +1471,8 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
             uint16_t* out = (uint16_t*)a.out + (int64_t)(lo + i) * a.ldo + (int64_t)head * D;
             float* po = p.part_o + part * D;
 #pragma unroll 1
-            for (int d = 0; d < D; d += 8) {
-                float o[8];
+            for (int d = 0; d < D; d += 16) {
+                float o[16];
                 tm_ld(at_o + d, o);
                 for (uint64_t b = badv; b; b &= b - 1) {
                     const int slot = len + __ffsll(b) - 1;
@@ -1480,22 +1480,24 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                                              ((((int64_t)a.layer * c.pages + trow[slot >> shift]) * c.kv_heads + g.h) *
                                                   c.page_size + (slot & (c.page_size - 1))) * D + d;
 #pragma unroll
-                    for (int j = 0; j < 8; ++j) {
+                    for (int j = 0; j < 16; ++j) {
                         const float x = __bfloat162float(v[j]);
                         if (!isfinite(x)) o[j] += x;
                     }
                 }
                 if (col < rows && whole) {
-                    uint32_t h[4];
+                    uint32_t h[8];
 #pragma unroll
-                    for (int j = 0; j < 8; j += 2) {
+                    for (int j = 0; j < 16; j += 2) {
                         const __nv_bfloat162 y = __floats2bfloat162_rn(o[j] * inv, o[j + 1] * inv);
                         h[j / 2] = *reinterpret_cast<const uint32_t*>(&y);
                     }
                     *reinterpret_cast<uint4*>(out + d) = make_uint4(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint4*>(out + d + 8) = make_uint4(h[4], h[5], h[6], h[7]);
                 } else if (col < rows) {
-                    *reinterpret_cast<float4*>(po + d) = make_float4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<float4*>(po + d + 4) = make_float4(o[4], o[5], o[6], o[7]);
+#pragma unroll
+                    for (int j = 0; j < 16; j += 4)
+                        *reinterpret_cast<float4*>(po + d + j) = make_float4(o[j], o[j + 1], o[j + 2], o[j + 3]);
                 }
                 __syncwarp();
             }
