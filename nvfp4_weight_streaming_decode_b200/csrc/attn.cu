@@ -37,6 +37,9 @@
 // non-finite values of drafted slots are zeroed there and added back at the
 // end to the rows that do see them.
 //
+// Lanes of more than 128 query rows to a cached head have a kernel of their own
+// (attn_wide_kernel, heads of 64 and 128), the other way round.
+//
 // What bounds it: memory, while a block has up to 64 rows or so; then the softmax
 // (a tile of 128 x 128 costs some 3,000 cycles, of which the exponentials alone
 // take 1,024, and the operands' way through shared memory about as much as the
@@ -45,8 +48,8 @@
 //   8 lanes x 1 row, 40 / 40 heads of 128, up to 4,000 slots   80 us  5.7 TB/s 0.87
 //   8 lanes x 8 rows, 40 / 8 heads of 128, up to 32,768 slots 125 us  5.9 TB/s 0.91
 //   5 lanes x 2-8 rows, 24 / 4 heads of 256, up to 20,011      57 us  4.9 TB/s 0.75
-//   1 lane x 64 rows, 64 / 8 heads of 128, 65,537 slots       176 us  0.78 PFLOP/s
 //   1 row, 40 / 8 heads, no context                           7.4 us
+//   1 lane x 64 rows, 64 / 8 heads of 128, 65,537 slots       136 us  1.01 PFLOP/s (attn_wide_kernel)
 //
 // Every wait is bounded; one that runs out flags the device status, stops the
 // CTA, waits (bounded) for copies and products in flight, frees the tensor
@@ -1179,7 +1182,21 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
 // and read) out of the shared memory's way.  A CTA has two halves of 128 rows,
 // four warps each.  Scores come in steps of 64 slots and two buffers, so that a half's warps
 // have the next scores while the tensor cores take up the weights of the last.
-// V is shared, so one more warp looks after its slots that rows must not see, ahead of the products.
+// V is shared, so one more warp looks after its slots that rows must not see, ahead
+// of the products.
+//
+// Measured against blocks of 128 rows in attn_kernel (64 query heads, 8 cached of
+// 128, one lane): 64 rows of 65,537 slots 136 us and 177, 32 rows 85 and 99, 20 rows
+// 82 and 98, 48 rows (a block and a half) 144 and 140; 64 rows of 4,000 slots 28.8 and
+// 28.8, 1,000 slots 24.1 and 26.5; 20 rows of 4,000 slots 23.8 and 23.1; heads of 64, 64 rows 118 and 177.
+// So any lane of more than 128 rows to a head comes here.
+//
+// Bound by the loop of weights, products and scores: a step of 64 slots for both
+// halves takes 1,860 cycles, the exponentials 1,024 of them and the products 1,024
+// (51 % of the tensor and of the exponential unit's cycles); leaving out the
+// exponentials changes nothing, leaving out the products 10 %.  Runs of some
+// milliseconds meet the power limit (160 us).  Not kept: a warp of products for each
+// half, waits that poll, other orders of the halves (140 to 146 us).
 template <int D>
 __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
     attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,
