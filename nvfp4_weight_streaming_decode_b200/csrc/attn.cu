@@ -495,6 +495,24 @@ __device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, 
 __device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
 
+// A reference is a rounded score, but scores are taken against it before their
+// rounding.  From 2^28 on the two may differ by 16 and more, and by any power of two in
+// the end.  Such a reference is rounded down, so that the largest score is not below
+// it, and log2 weights are cut at kMostLog: a cut one is within the rounding of its score of the largest.
+constexpr float kBig = 268435456.f, kMostLog = 64.f;
+__device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= kBig && fabsf(m) < -kUnseen; }
+__device__ __forceinline__ float reference_of(float top)
+{
+    return fmaxf(is_big(top) ? fmaf(-fabsf(top), 1.1920929e-07f, top) : top, kUnseen);
+}
+template <int C>
+__device__ __forceinline__ void cut(float (&x)[C])
+{
+#pragma unroll
+    for (int i = 0; i < C; ++i)
+        if (x[i] > kMostLog) x[i] = kMostLog;  // (NaN stays)
+}
+
 // C scores of this thread's slot from tensor memory, as log2 weights against the
 // references: x = s scale log2(e) - m.  Masked ones are -inf, whatever the
 // scale's sign.  `plain`: the whole warp's slots are seen by every row; `all`:
@@ -588,31 +606,36 @@ __device__ __forceinline__ void join_columns(const float (&x)[C], int lane, floa
 
 // The first tile of a segment: its columns' maxima become the references, and
 // the scores (read with references of 0) are taken against them.  A column
-// that sees nothing yet stays unseen.
+// that sees nothing yet stays unseen.  Returns whether a reference is a big one.
 template <int C>
-__device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
+__device__ __forceinline__ bool first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
 {
+    bool big = false;
     join_columns<C>(x, lane, s.red[quad] + c0, [](float a, float b) { return fmaxf(a, b); });
     any_of(bar, 128, false);
     if (quad * 32 + lane < C) {
         const int col = c0 + quad * 32 + lane;
         const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-        s.neg_m[col] = -fmaxf(top, kUnseen);
+        s.neg_m[col] = -reference_of(top);
+        big = is_big(top);
     }
-    any_of(bar, 128, false);
+    big = any_of(bar, 128, big);
 #pragma unroll
     for (int i = 0; i < C; i += 4) {
         const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(s.neg_m + c0 + i);
         unpair(add2(pair(x[i], x[i + 1]), m.x), x[i], x[i + 1]);
         unpair(add2(pair(x[i + 2], x[i + 3]), m.y), x[i + 2], x[i + 3]);
     }
+    if (big) cut<C>(x);
+    return big;
 }
 
 
 // This group of four warps gives its columns the maxima of this tile's scores as
-// references where those are higher, and scales its sums and O^T so far.
+// references where those are higher, and scales its sums and O^T so far.  Returns
+// whether a reference is a big one.
 template <int D, int N>
-__device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bool plain, bool all, uint64_t bit, float sl,
+__device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bool plain, bool all, uint64_t bit, float sl,
                                      int c0, int quad, int lane, int bar, bool started, f32x2 (&l)[N / 4],
                                      uint32_t pfree, uint32_t parity, volatile int* abort, bool& fail)
 {
@@ -643,8 +666,8 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
         for (int j = 0; j < 8; ++j) {
             const int col = c0 + i0 + j;
             const float was = -s.neg_m[col];
-            float now = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-            now = fmaxf(now, was);
+            const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+            const float now = fmaxf(reference_of(top), was);
             down[j] = was == now ? 1.f : fast_exp2(was - now);
         }
 #pragma unroll
@@ -669,10 +692,14 @@ __device__ __forceinline__ void rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
     fence_before();
     any_of(bar, 128, false);  // every thread has read the old references
     const int col = c0 + quad * 32 + lane;
-    if (quad * 32 + lane < C)
-        s.neg_m[col] = -fmaxf(-s.neg_m[col], fmaxf(fmaxf(s.red[0][col], s.red[1][col]),
-                                                   fmaxf(s.red[2][col], s.red[3][col])));
-    any_of(bar, 128, false);
+    bool big = false;
+    if (quad * 32 + lane < C) {
+        const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+        const float now = fmaxf(-s.neg_m[col], reference_of(top));
+        s.neg_m[col] = -now;
+        big = is_big(now);
+    }
+    return any_of(bar, 128, big);
 }
 
 // ------------------------------------------------- what both kernels share
@@ -967,7 +994,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             f32x2 l[C / 2];
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) l[i] = 0;
-            bool stop = false;
+            bool stop = false, big = false;
             for (int t = 0; t < n; ++t) {
                 const int T = done + t, sb = T & 1, pb = T % L::kPBufs;
                 const int slot = (g.t0 + t) * kTile + srow;
@@ -982,7 +1009,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fence_after();
                 float x[C];
                 read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
-                if (t == 0) first_references<C>(s, x, c0, quad, lane, bar);
+                if (t == 0)
+                    big = first_references<C>(s, x, c0, quad, lane, bar);
+                else if (big)
+                    cut<C>(x);
                 // Two buffers of P: S of this tile was issued after O of the tile before the
                 // last, so once S is there the weights of that tile are done with.
                 if (L::kPBufs == 1 && T > 0) fail = fail || !waitw(smem_addr(&s.pfree[0]), (T - 1) & 1, abort);
@@ -996,9 +1026,10 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                         stop = true;
                         break;
                     }
-                    rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
+                    big = rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
                                smem_addr(&s.pfree[(T + L::kPBufs - 1) % L::kPBufs]), ((T - 1) / L::kPBufs) & 1, abort, fail);
                     read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
+                    if (big) cut<C>(x);
                     weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
                 }
 #pragma unroll
@@ -1139,7 +1170,7 @@ __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, cons
 
 // A row's weights as packed bf16 pairs; returns their sum (before the rounding).
 __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[2],
-                                           uint32_t (&w)[32])
+                                           bool big, uint32_t (&w)[32])
 {
     f32x2 s0 = 0, s1 = 0;
     float buf[2][32];
@@ -1155,6 +1186,7 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
             tm_ld16(at + 48, buf[1] + 16);
         }
         log2_weights(x, sl, neg_m, plain, seen[z]);
+        if (big) cut<32>(x);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
 #pragma unroll
@@ -1403,6 +1435,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
             };
             pages_of(0);
             float neg_m = 0.f, l = 0.f;
+            bool big = false;  // a reference of the warp's is
             for (int st = 0; st < steps; ++st) {
                 const int slot0 = g.t0 * kTile + st * kStep, S = did + st;
                 const uint32_t at_s = at_half + S % 2 * kStep;
@@ -1439,11 +1472,12 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
 #pragma unroll 1
                 for (int turn = 0; turn < 2; ++turn) {
                     if (__any_sync(0xffffffffu, rise)) {
-                        const float was = st == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
-                        const float now = rise ? fmaxf(top, was) : was;
+                        const float was = st == 0 && turn == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
+                        const float now = rise ? fmaxf(reference_of(top), was) : was;
                         const float down = was == now ? 1.f : fast_exp2(was - now);
                         l *= down;
                         neg_m = -now;
+                        big = __any_sync(0xffffffffu, is_big(now));
                         if (st > 0) {
                             // O so far, once the step before is in (S waited for the one before that)
                             ok = ok && waitw(smem_addr(&s.pfree[half]), (S - 1) & 1, abort);
@@ -1458,7 +1492,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                             }
                         }
                     }
-                    sum = weigh_row(at_s, sl, neg_m, plain, seen, w);
+                    sum = weigh_row(at_s, sl, neg_m, plain, seen, big, w);
                     rise = sum > kMostWeight;
                     if (!__any_sync(0xffffffffu, rise)) break;
                 }

@@ -344,6 +344,22 @@ def test_wide_sharp_and_flat_scores(dev, scale, spread):
     check(dev, 44, [900], [40], 8, 2, 128, 64, scale=scale, spread=spread)
 
 
+@pytest.mark.parametrize("power", [22, 26, 33, 60])
+@pytest.mark.parametrize("rows", [3, 40])
+@pytest.mark.parametrize("n", [0, 300, 9000])
+def test_scores_past_the_headroom_s_own_rounding(dev, n, rows, power):
+    """Scores of some 2^power for every second row: their rounding alone may pass 2^32; between rows of ordinary ones."""
+    rng = np.random.default_rng(51)
+    c, r = ch.make(dev, 51, [n], [rows], hkv=2, page=64, dim=128)
+    x = rng.standard_normal((rows, 8, 128))
+    x[::2] *= 2.0**power
+    q = ch.dev_bf16(cache_ref.bf16_bits(x), dev)
+    out, lse = abi.attn_tree(c, 0, q, 0.1, row_start=ch.ints([0, rows], dev), max_nodes=rows, want_lse=True)
+    torch.cuda.synchronize()
+    assert torch.isfinite(out).all() and torch.isfinite(lse).all()
+    compare(c, r, q, 0.1, [0, rows], None, out, lse)
+
+
 @pytest.mark.parametrize("scale", [0.25, -0.25, 40.0])
 def test_wide_running_maximum(dev, scale):
     """Every tile has a new maximum, for every second row; the others' scores fall."""
