@@ -706,20 +706,31 @@ def beam_select(logits, scores, vocab=None, finished=None, eos=-1, scores_out=No
     f32, i32, u8 = torch.float32, torch.int32, torch.uint8
     shape = (groups, beams)
     sp = _want(scores, "scores", f32, dev, shape)
+    # (what is allocated here needs no check: 0.5 us each)
     if scores_out is None:
         scores_out = torch.empty_like(scores)
+        op = scores_out.data_ptr()
+    else:
+        op = _want(scores_out, "scores_out", f32, dev, shape)
     if parent is None:
         parent = torch.empty_like(scores, dtype=i32)
+        pp = parent.data_ptr()
+    else:
+        pp = _want(parent, "parent", i32, dev, shape)
     if token is None:
         token = torch.empty_like(scores, dtype=i32)
+        tp = token.data_ptr()
+    else:
+        tp = _want(token, "token", i32, dev, shape)
     if finished_out is None:
         finished_out = torch.empty_like(scores, dtype=u8)
+        dp = finished_out.data_ptr()
+    else:
+        dp = _want(finished_out, "finished_out", u8, dev, shape)
     if workspace is None:
         workspace = beam_select_workspace(groups, beams, V, dev)
     _call("nvfp4_beam_select", dev, None, logits.data_ptr(), groups, beams, V, ldv, sp,
-          _want(finished, "finished", u8, dev, shape), eos, _want(scores_out, "scores_out", f32, dev, shape),
-          _want(parent, "parent", i32, dev, shape), _want(token, "token", i32, dev, shape),
-          _want(finished_out, "finished_out", u8, dev, shape), _want(workspace, "workspace", u8, dev),
+          _want(finished, "finished", u8, dev, shape), eos, op, pp, tp, dp, _want(workspace, "workspace", u8, dev),
           workspace.shape[0])
     return scores_out, parent, token, finished_out
 
