@@ -383,20 +383,23 @@ typedef struct {
  * Every lane i takes lane parent[i]'s pages and length: beams reordered after
  * a selection (nvfp4_beam_select's parents), sequences forked, lanes freed
  * (parent[i] = -1: the lane is emptied).  parent: device int32 [lanes].  Only
- * tables, lengths and reference counts change; pages are shared, and the last,
- * partly filled one is copied by nvfp4_cache_reserve before it is written.
+ * tables, lengths and reference counts change; pages are shared, reserved ones
+ * too, and nvfp4_cache_reserve gives a lane its own before it writes.
  * A parent outside -1..lanes-1 counts as -1 (and sets the status bit).
  * One asynchronous launch.
  */
 NVFP4_API int nvfp4_cache_fork(const nvfp4_cache* cache, const int32_t* parent, nvfp4_stream_t stream);
 
 /*
- * Room for want[b] more slots behind len[b], for every lane: pages are added
- * where the lane has none (reference count 1), and where want[b] > 0 and the
- * lane's last page is partly filled and shared, its filled slots are copied,
- * in every layer, to a page of the lane's own (lanes in order; the last holder
- * keeps the page).  Pages are taken lowest id first, lane by lane, a lane's
- * copy before its new pages.  want: device int32 [lanes], <= 0: nothing.
+ * Room for want[b] more slots behind len[b], for every lane: where want[b] > 0,
+ * every page under the slots len[b] .. len[b] + want[b] - 1 becomes the lane's
+ * own.  Pages are added where the lane has none (reference count 1); one that is
+ * shared (after a fork, or by a reference of the caller's) is replaced, lanes in
+ * order, and the last holder keeps it.  Of a partly filled last page the filled
+ * slots are copied, in every layer; slots behind len[b] hold nothing committed
+ * and are not (drafts in a page that is replaced are lost).  Pages are taken
+ * lowest id first, lane by lane, a lane's in the order of its slots.  want:
+ * device int32 [lanes], <= 0: nothing.
  * All or nothing: if the pool has too few free pages, or a lane would pass
  * max_pages, nothing changes, bit 256 of nvfp4_device_status() is set and *ok
  * is 0 (else 1).  ok: device int32, or NULL.  One asynchronous launch.

@@ -544,7 +544,7 @@ class Cache:
         _call("nvfp4_cache_fork", self.device, stream, self._ref, pp)
 
     def reserve(self, want, ok=None, stream=None):
-        """Room for want[b] more slots in each lane; shared last pages are copied.
+        """Room for want[b] more slots in each lane, in pages of its own: shared ones are copied or replaced.
         ok: int32 [1], set to 0 if the pool had too few free pages."""
         import torch
         wp, op = self._lanes(want, "want"), _want(ok, "ok", torch.int32, self.device, (1,))

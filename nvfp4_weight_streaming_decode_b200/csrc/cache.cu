@@ -66,13 +66,13 @@ __global__ void __launch_bounds__(kForkThreads) fork_kernel(const nvfp4_cache c,
 // ------------------------------------------------------------- reserve
 // One launch plans, copies and applies.  Every CTA reads the same inputs and
 // comes to the same plan: how many pages each lane takes (a copy of its shared
-// last page, then the missing entries up to len + want); the n-th page taken is
-// the n-th free one.
-//   No copies: CTA 0 applies the plan.  A CTA that reads later, when tables have
-//   changed, still finds nothing to copy (no count of a last page changes).
-//   Copies: every CTA counts in when it has read all it needs, copies its share
-//   of the filled slots -- per (layer, k or v, head) one contiguous run -- and
-//   the last to count in applies the plan.
+// last page, then, up to len + want, one for each shared entry and each missing
+// one); the n-th page taken is the n-th free one.
+//   Nothing shared: CTA 0 applies the plan.  A CTA that reads later, when tables
+//   have changed, still finds nothing shared (the new entries' counts are 1).
+//   Shared pages: every CTA counts in when it has read all it needs, copies its
+//   share of the last pages' filled slots -- per (layer, k or v, head) one
+//   contiguous run -- and the last to count in applies the plan.
 constexpr int kResThreads = 512;
 constexpr int kResWarps = kResThreads / 32;
 constexpr int kResStep = 8 * kResThreads;  // page ids looked at in one step
@@ -80,15 +80,38 @@ constexpr int kResStep = 8 * kResThreads;  // page ids looked at in one step
 struct Plan {
     int need[kMaxLanes], first[kMaxLanes], copy[kMaxLanes], last[kMaxLanes], dst[kMaxLanes], fill[kMaxLanes],
         col[kMaxLanes];
+    int lo[kMaxLanes];         // [lo, first): entries behind the length that are there
+    int shared[kMaxLanes];     // of those, the ones to replace
+    int at[kMaxLanes];         // the next entry to look at when they are
     int start[kMaxLanes + 1];  // pages taken before lane b
+    int ids[kResStep];         // the free pages of a step, where entries are replaced
     int count[kResWarps];
-    int bad, copies, last_in;
+    int bad, copies, replaces, last_in;
 };
 
+// Whether lane b gives up page p, in its column col: another holder is left when the
+// lanes before b that hold it too, where they ask for room, have had their turn.
+__device__ __forceinline__ bool gives_up(const nvfp4_cache& c, const Plan& s, int b, int col, int p)
+{
+    if (p >= c.pages) return false;
+    const int r = c.ref[p];
+    if (r <= 1) return false;
+    int before = 0;
+#pragma unroll 8
+    for (int o = 0; o < b; ++o) {  // (loads in flight together)
+        const bool in = col >= s.lo[o] && col < s.first[o];
+        const int held = in ? c.table[(int64_t)o * c.max_pages + col] : -1;
+        before += s.last[o] == p || held == p;
+    }
+    return r - before > 1;
+}
+
 // Walk the free pages in order of their ids, until `total` of them have gone
-// by: take(rank, page) for each.  Returns whether there are so many (all threads).
-template <class Take>
-__device__ bool walk_free(const nvfp4_cache& c, int total, Plan& s, Take take)
+// by: take(rank, page, before) for each, then, for the whole CTA, step(before,
+// after) with the ranks that a step's pages have.  Returns whether there are so
+// many (all threads).
+template <class Take, class Step>
+__device__ bool walk_free(const nvfp4_cache& c, int total, Plan& s, Take take, Step step)
 {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int given = 0;
@@ -120,7 +143,8 @@ __device__ bool walk_free(const nvfp4_cache& c, int total, Plan& s, Take take)
         before = __shfl_sync(0xffffffffu, all - before, warp);
         all = __shfl_sync(0xffffffffu, all, kResWarps - 1);
         int rank = given + before + incl - n;
-        for (; free && rank < total; free &= free - 1) take(rank++, p0 + __ffs(free) - 1);
+        for (; free && rank < total; free &= free - 1) take(rank++, p0 + __ffs(free) - 1, given);
+        step(given, min(given + all, total));
         given += all;
         __syncthreads();
     }
@@ -172,15 +196,19 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
     if (tid == 0) {
         s.bad = 0;
         s.copies = 0;
+        s.replaces = 0;
     }
     if (tid < kMaxLanes) {
+        s.lo[tid] = 0;
+        s.first[tid] = 0;
+        s.shared[tid] = 0;
         s.need[tid] = 0;
         s.copy[tid] = 0;
         s.last[tid] = -1;
         s.dst[tid] = -1;
     }
     __syncthreads();
-    // a warp per lane: the missing entries, and the count of a partly filled last page
+    // a warp per lane: the missing entries, and its partly filled last page
     for (int b = warp; b < c.lanes; b += kResWarps) {
         const int w = want[b], n = max(c.len[b], 0);
         if (w <= 0) continue;
@@ -204,13 +232,13 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
         }
         if (lane == 0) {
             s.need[b] = c1 - first;
+            s.lo[b] = s.at[b] = c0;
             s.first[b] = first;
             s.fill[b] = n & (c.page_size - 1);
             s.col[b] = n >> shift;
             if (partly) {
                 if (p >= 0 && p < c.pages) {
                     s.last[b] = p;
-                    s.copy[b] = c.ref[p];
                 } else if (blockIdx.x == 0) {
                     atomicOr(&g_cache_status, kRefused);
                 }
@@ -218,17 +246,23 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
         }
     }
     __syncthreads();
-    // which lanes copy their last page: in lane order, all but the last holder
-    int mine = 0;
-    if (tid < kMaxLanes && s.last[tid] >= 0) {
-        int before = 0;
-        for (int b = 0; b < tid; ++b) before += s.last[b] == s.last[tid];
-        mine = s.copy[tid] - before > 1;
+    // what of it is shared, in lane order: all but the last holder take a page of their own
+    if (tid < kMaxLanes && s.last[tid] >= 0 && gives_up(c, s, tid, s.col[tid], s.last[tid])) {
+        s.copy[tid] = 1;
+        s.copies = 1;
     }
-    __syncthreads();
-    if (tid < kMaxLanes) {
-        s.copy[tid] = mine;
-        if (mine) s.copies = 1;
+    for (int b = warp; b < c.lanes; b += kResWarps) {
+        const int32_t* row = c.table + (int64_t)b * c.max_pages;
+        int n = 0;
+        for (int q = s.lo[b]; q < s.first[b]; q += 32) {
+            const int col = q + lane;
+            n += __popc(__ballot_sync(0xffffffffu, col < s.first[b] && gives_up(c, s, b, col, row[col])));
+        }
+        if (lane == 0 && n) {
+            s.shared[b] = n;
+            s.need[b] += n;
+            s.replaces = 1;
+        }
     }
     __syncthreads();
     if (warp == 0) {
@@ -249,13 +283,18 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
     const int total = s.start[kMaxLanes];
     bool enough = !s.bad && total <= c.pages, apply = blockIdx.x == 0;
     unsigned* counter = (unsigned*)c.scratch + 4 * c.lanes;
-    if (s.copies) {
-        if (enough)
-            enough = walk_free(c, total, s, [&](int rank, int page) {
-                int b = 0;
-                while (s.start[b + 1] <= rank) ++b;
+    auto no_step = [](int, int) {};
+    auto lane_of = [&](int rank) {
+        int b = 0;
+        while (s.start[b + 1] <= rank) ++b;
+        return b;
+    };
+    if (s.copies || s.replaces) {
+        if (enough && s.copies)
+            enough = walk_free(c, total, s, [&](int rank, int page, int) {
+                const int b = lane_of(rank);
                 if (s.copy[b] && rank == s.start[b]) s.dst[b] = page;
-            });
+            }, no_step);
         __syncthreads();
         if (tid == 0) s.last_in = count_in(counter) == gridDim.x - 1;
         __syncthreads();
@@ -264,20 +303,68 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
     }
     if (!apply) return;
     if (enough)
-        enough = walk_free(c, total, s, [](int, int) {});
-    if (enough)
-        walk_free(c, total, s, [&](int rank, int page) {
-            int b = 0;
-            while (s.start[b + 1] <= rank) ++b;
+        enough = walk_free(c, total, s, [](int, int, int) {}, no_step);
+    if (enough && !s.replaces) {
+        walk_free(c, total, s, [&](int rank, int page, int) {
+            const int b = lane_of(rank);
             const int nth = rank - s.start[b] - s.copy[b];
             c.table[(int64_t)b * c.max_pages + (nth < 0 ? s.col[b] : s.first[b] + nth)] = page;
             c.ref[page] = 1;
+        }, no_step);
+    } else if (enough) {
+        // The entries to replace, marked -2 - page, from the last lane to the first:
+        // a lane's are known by the entries of the lanes before it.
+        for (int b = c.lanes - 1; b >= 0; --b) {
+            if (!s.shared[b]) continue;
+            int32_t* row = c.table + (int64_t)b * c.max_pages;
+            for (int q = s.lo[b] + tid; q < s.first[b]; q += kResThreads) {
+                const int p = row[q];
+                if (gives_up(c, s, b, q, p)) row[q] = -2 - p;
+            }
+            __syncthreads();
+        }
+        // A step's free pages in order; a warp per lane gives its entries theirs.
+        walk_free(c, total, s, [&](int rank, int page, int before) { s.ids[rank - before] = page; },
+                  [&](int r0, int r1) {
+            __syncthreads();
+            for (int b = warp; b < c.lanes; b += kResWarps) {
+                int r = max(s.start[b], r0);
+                const int end = min(s.start[b + 1], r1);
+                if (r >= end) continue;
+                int32_t* row = c.table + (int64_t)b * c.max_pages;
+                if (s.copy[b] && r == s.start[b]) {
+                    if (lane == 0) {
+                        row[s.col[b]] = s.ids[r - r0];
+                        c.ref[s.ids[r - r0]] = 1;
+                    }
+                    ++r;
+                }
+                int q = s.at[b];
+                while (r < end && q < c.max_pages) {
+                    const int col = q + lane, e = col < s.first[b] ? row[col] : -1;
+                    const unsigned m = __ballot_sync(0xffffffffu, e < 0);
+                    const int mine = r + __popc(m & ((1u << lane) - 1));
+                    const bool takes = e < 0 && mine < end && col < c.max_pages;
+                    if (takes) {
+                        const int page = s.ids[mine - r0];
+                        row[col] = page;
+                        c.ref[page] = 1;
+                        if (e < -1) atomicSub(c.ref + (-2 - e), 1);
+                    }
+                    const unsigned done = __ballot_sync(0xffffffffu, takes);
+                    r += __popc(done);
+                    q = done == m ? q + 32 : q + 32 - __clz(done);
+                }
+                __syncwarp();
+                if (lane == 0) s.at[b] = q;
+            }
         });
+    }
     if (enough && tid < c.lanes && s.copy[tid]) atomicSub(c.ref + s.last[tid], 1);
     if (tid == 0) {
         if (ok) *ok = enough ? 1 : 0;
         if (!enough) atomicOr(&g_cache_status, kNoPages);
-        if (s.copies) *counter = 0u;
+        if (s.copies || s.replaces) *counter = 0u;
     }
 }
 

@@ -51,21 +51,20 @@ class RefCache:
                 if w <= 0:
                     continue
                 n = int(self.len[b])
-                if n % self.page:
-                    p = self.table[b, n // self.page]
-                    if self.ref[p] > 1:
-                        d = take()
-                        copies.append((p, d, n % self.page))
-                        self.ref[p] -= 1
-                        self.ref[d] = 1
-                        self.table[b, n // self.page] = d
-                for col in range(-(-n // self.page), -(-(n + int(w)) // self.page)):
+                # the pages under the slots n .. n + w - 1
+                for col in range(n // self.page, -(-(n + int(w)) // self.page)):
                     if col >= self.table.shape[1]:
                         raise MemoryError
-                    if self.table[b, col] < 0:
-                        d = take()
-                        self.ref[d] = 1
-                        self.table[b, col] = d
+                    p = self.table[b, col]
+                    if p >= 0 and self.ref[p] <= 1:
+                        continue  # the lane's own already
+                    d = take()
+                    if p >= 0:
+                        if n > col * self.page:
+                            copies.append((p, d, n - col * self.page))
+                        self.ref[p] -= 1
+                    self.ref[d] = 1
+                    self.table[b, col] = d
         except MemoryError:
             self.table, self.ref = saved
             return False
