@@ -45,6 +45,7 @@ NVFP4_ROPE_HALVES = 0
 NVFP4_ROPE_ADJACENT = 1
 NVFP4_ATTN_MAX_ROWS = 64
 NVFP4_MAX_M = 64          # nvfp4_gemm_decode: 1..8 decode lanes, 9..64 verify rows
+NVFP4_ROUND_ROWS = 8      # rows of a round's widest graph
 
 _P = ctypes.c_void_p
 _I64 = ctypes.c_int64
@@ -822,13 +823,29 @@ def _between(kind, record, *keep):
     return d
 
 
+def _round_rows(t, name):
+    """A round keeps the tensor's address and runs at widths of up to 8 rows: it is the caller's, and has them all."""
+    if t is None:
+        raise ValueError(f"{name} must be given: a round's nodes keep its address")
+    if t.dim() < 2 or t.shape[0] < NVFP4_ROUND_ROWS:
+        raise ValueError(f"{name} must have {NVFP4_ROUND_ROWS} rows, the widest round's: got {tuple(t.shape)}")
+
+
 def desc_rope(cache, layer, y, q_heads, inv_freq, positions, q, pair_axis=None, style=NVFP4_ROPE_HALVES):
-    """An Nvfp4GemmDesc of a round's rotary append (rope_append's arguments, one row per lane, 8 rows)."""
+    """An Nvfp4GemmDesc of a round's rotary append: rope_append's arguments with one row per lane, 8 rows, q given.  The
+    tensors are kept with the descriptor and must outlive the round."""
+    _round_rows(y, "y")
+    _round_rows(q, "q")
     record, _ = _rope_record(cache, layer, y, q_heads, inv_freq, positions, pair_axis, style, None, q)
     return _between(NVFP4_DESC_ROPE_APPEND, record, cache, y, inv_freq, positions, q, pair_axis)
 
 
 def desc_attn(cache, layer, q, scale, out, workspace, lse=None):
-    """An Nvfp4GemmDesc of a round's attention (attn_tree's arguments, one row per lane, 8 rows)."""
+    """An Nvfp4GemmDesc of a round's attention: attn_tree's arguments with one row per lane, 8 rows, out and workspace
+    given.  The tensors are kept with the descriptor and must outlive the round."""
+    _round_rows(q, "q")
+    _round_rows(out, "out")
+    if workspace is None:
+        raise ValueError("workspace must be given: a round's nodes keep its address")
     record = _attn_record(cache, layer, q, scale, None, None, 1, out, False, lse, workspace)[0]
     return _between(NVFP4_DESC_ATTN_TREE, record, cache, q, out, workspace, lse)
