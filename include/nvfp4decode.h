@@ -491,6 +491,9 @@ NVFP4_API int nvfp4_rope_append(const nvfp4_rope_args* args, nvfp4_stream_t stre
  *   lse     float [rows][q_heads], or NULL
  * Rows at or behind row_start[lanes] are left as they were.  Sums are held in
  * FP32; the weights exp(s - max) are rounded to bf16 for the product with v.
+ * Finite scores and values give finite results for up to 65,536 visible slots,
+ * and for more where no |v| passes 2^113.  Weights below 2^-102 of the largest
+ * count as zero, and values below 2^-102 lose bits.
  *
  * Limits: 1 <= rows <= NVFP4_ATTN_MAX_ROWS, the verify width (NVFP4_ERR_M);
  * q_heads a multiple of kv_heads and at most 32 times it, 0 <= layer < layers,

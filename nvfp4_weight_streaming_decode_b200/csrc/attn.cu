@@ -12,12 +12,15 @@
 // columns instead of a padded tile of rows: one row and eight drafts run the
 // same code at the same memory rate.
 //
-// The reference m of a column is the maximum of a segment's first tile (or the
-// first to show it a slot), not the running maximum: weights up to 2^kHeadroom are as exact in
-// FP32 and bf16 as weights below 1 (both hold powers of two that far), so
-// O^T is rescaled only when a score passes m by more than that -- rarely, by a
-// vote of the 128 threads that share the columns.  The weights' one rounding to
-// bf16 is the tensor cores' operand type; their sums are taken before it.
+// The reference m of a column is 24 above the maximum of a segment's first tile
+// (or of the first to show it a slot), in log2, not above the running maximum: FP32
+// and bf16 hold a weight as exactly at 2^-24 as at 1.  O^T is rescaled only when a
+// weight passes 2^-16 -- rarely, by a vote of the 128 threads that share the columns.
+// So no weight is above 2^-16, and 65,536 slots of the largest bf16 value still sum
+// to a finite O^T (with weights up to 2^32, as far as they are exact too, values
+// from 2^96 on overflowed).  What that costs lies below: weights 2^-102 of the largest are
+// zero, and values below 2^-102 lose bits.  The weights' one rounding to bf16 is
+// the tensor cores' operand type; their sums are taken before it.
 //
 // Split: the tiles of all (lane, cached head) pairs form one line that the
 // grid's CTAs share evenly (ragged lanes balance by themselves).  A pair cut
@@ -75,8 +78,10 @@ namespace {
 constexpr unsigned kBadPage = 1u, kGaveUp = 4u;
 constexpr int kTile = 128;                 // slots per tile
 constexpr int kMaxLanes = NVFP4_CACHE_MAX_LANES;
-constexpr float kHeadroom = 32.f;          // weights up to 2^32 before a rescale; their sums stay far below 2^127
-constexpr float kMostWeight = 4294967296.f;  // 2^kHeadroom
+constexpr float kAbove = 24.f;             // a reference lies this far above its score, in log2
+constexpr float kUp = 16777216.f;          // 2^kAbove
+constexpr float kMostLog = -16.f;          // a score with more than this against its reference raises it
+constexpr float kMostWeight = 1.f / 65536;  // 2^kMostLog
 constexpr float kUnseen = -3.0e38f;        // reference of a column that has seen no slot
 constexpr uint32_t kSleepNs = 1000;
 constexpr uint32_t kPolls = 1u << 20;      // about a second
@@ -137,7 +142,8 @@ struct Shared {  // at kOffMisc
     Lanes lanes;
     uint64_t vis[128];                 // drafted slots each column sees
     alignas(16) float neg_m[128];      // each column's reference, negated
-    float inv[128];                    // 1 / sum
+    uint8_t raw[128];                  // whether it is a raw score
+    float inv[128];                    // 1 / sum; before, while references rise, the factor of what was weighed so far
     int64_t off[128];                  // where each column's output row starts
     int lse[128];
     float red[4][128];
@@ -148,7 +154,7 @@ struct AttnParams {
     nvfp4_cache c;
     nvfp4_attn_args a;
     float* part_o;       // [ctas][2][N][D]
-    float2* part_ml;     // [ctas][2][N]
+    float2* part_ml;     // [ctas][2][N]: reference and sum, negative where the reference is a raw score
     int ctas;            // of the attention kernel
     int per_block;       // rows of a lane per block: as many whole rows (of G columns) as fit N
     int q_box;           // rows a copy of Q brings (at most per_block)
@@ -495,31 +501,50 @@ __device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, 
 __device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
 
-// A reference is a rounded score, but scores are taken against it before their
-// rounding.  From 2^28 on the two may differ by 16 and more, and by any power of two in
-// the end.  Such a reference is rounded down, so that the largest score is not below
-// it, and log2 weights are cut at kMostLog: a cut one is within the rounding of its score of the largest.
-constexpr float kBig = 268435456.f, kMostLog = 64.f;
-__device__ __forceinline__ bool is_big(float m) { return fabsf(m) >= kBig && fabsf(m) < -kUnseen; }
-__device__ __forceinline__ float reference_of(float top)
+// A log2 weight is s sl - m, one rounding; but m is a rounded score, and so is s sl
+// where the first tile's maximum is looked for.  From kRaw on, where that would
+// show (by 2^-12), a reference is a raw score r (before the scale) instead:
+// the weight is (s - r) sl - kAbove, and s - r is exact for the scores that count.
+constexpr float kRaw = 4096.f;
+__device__ __forceinline__ bool is_raw(float top) { return fabsf(top) >= kRaw && fabsf(top) < -kUnseen; }
+__device__ __forceinline__ float raw_weight(float s, float neg_r, float sl) { return (s + neg_r) * sl - kAbove; }
+
+// A column's reference: -m, or -r where raw.
+struct Reference {
+    float neg;
+    bool raw;
+};
+
+// The reference `was` raised to the score whose u = s sign(sl) is `top`, where that lies
+// higher; down: the log2 factor of what has been weighed so far.
+__device__ __forceinline__ Reference raised(Reference was, float top, float sl, float& down)
 {
-    return fmaxf(is_big(top) ? fmaf(-fabsf(top), 1.1920929e-07f, top) : top, kUnseen);
+    const float mag = fabsf(sl), u = sl < 0.f ? was.neg : -was.neg;  // (of a raw one)
+    const float at = top * mag;
+    down = 0.f;
+    if (was.raw ? !(top > u) : !(at + kAbove > -was.neg)) return was;
+    const Reference now = is_raw(at) ? Reference{sl < 0.f ? top : -top, true} : Reference{-(at + kAbove), false};
+    if (was.raw)
+        down = now.raw ? (u - top) * mag : fmaf(u, mag, now.neg) + kAbove;
+    else
+        down = now.raw ? -(fmaf(top, mag, was.neg) + kAbove) : now.neg - was.neg;
+    return now;
 }
-template <int C>
-__device__ __forceinline__ void cut(float (&x)[C])
+
+// Log-sum-exp of weights that sum to `sum` against a reference.
+__device__ __forceinline__ float log_sum(float sum, Reference m, float sl)
 {
-#pragma unroll
-    for (int i = 0; i < C; ++i)
-        if (x[i] > kMostLog) x[i] = kMostLog;  // (NaN stays)
+    if (sum == 0.f) return -INFINITY;
+    return (log2f(sum * kUp) + (m.raw ? -m.neg * sl : -m.neg - kAbove)) * 0.6931471805599453f;
 }
 
 // C scores of this thread's slot from tensor memory, as log2 weights against the
 // references: x = s scale log2(e) - m.  Masked ones are -inf, whatever the
 // scale's sign.  `plain`: the whole warp's slots are seen by every row; `all`:
-// this slot is.
+// this slot is.  `some_raw`: a column's reference is a raw score.
 template <int C>
 __device__ __forceinline__ void read_scores(uint32_t at, float (&x)[C], bool plain, bool all, uint64_t bit, float sl,
-                                            const uint64_t* vis, const float* neg_m)
+                                            const uint64_t* vis, const float* neg_m, bool some_raw, const uint8_t* raw)
 {
     tm_ld<C>(at, x);
     const f32x2 f = pair(sl, sl);
@@ -528,6 +553,16 @@ __device__ __forceinline__ void read_scores(uint32_t at, float (&x)[C], bool pla
         const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(neg_m + i);
         unpair(fma2(pair(x[i], x[i + 1]), f, m.x), x[i], x[i + 1]);
         unpair(fma2(pair(x[i + 2], x[i + 3]), f, m.y), x[i + 2], x[i + 3]);
+    }
+    if (some_raw) {  // (reads again what it needs: kept apart, so that the common path has its registers)
+#pragma unroll
+        for (int i = 0; i < C; i += 8) {
+            float y[8];
+            tm_ld(at + i, y);
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (raw[i + j]) x[i + j] = raw_weight(y[j], neg_m[i + j], sl);
+        }
     }
     if (!plain) {
 #pragma unroll
@@ -606,34 +641,30 @@ __device__ __forceinline__ void join_columns(const float (&x)[C], int lane, floa
 
 // The first tile of a segment: its columns' maxima become the references, and
 // the scores (read with references of 0) are taken against them.  A column
-// that sees nothing yet stays unseen.  Returns whether a reference is a big one.
+// that sees nothing yet stays unseen, and so does one whose reference has to be a raw
+// score: its weights then show as too large, and rise() sees to it.
 template <int C>
-__device__ __forceinline__ bool first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
+__device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
 {
-    bool big = false;
     join_columns<C>(x, lane, s.red[quad] + c0, [](float a, float b) { return fmaxf(a, b); });
     any_of(bar, 128, false);
     if (quad * 32 + lane < C) {
         const int col = c0 + quad * 32 + lane;
         const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-        s.neg_m[col] = -reference_of(top);
-        big = is_big(top);
+        s.neg_m[col] = -(is_raw(top) ? kUnseen : fmaxf(top + kAbove, kUnseen));
     }
-    big = any_of(bar, 128, big);
+    any_of(bar, 128, false);
 #pragma unroll
     for (int i = 0; i < C; i += 4) {
         const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(s.neg_m + c0 + i);
         unpair(add2(pair(x[i], x[i + 1]), m.x), x[i], x[i + 1]);
         unpair(add2(pair(x[i + 2], x[i + 3]), m.y), x[i + 2], x[i + 3]);
     }
-    if (big) cut<C>(x);
-    return big;
 }
 
-
-// This group of four warps gives its columns the maxima of this tile's scores as
-// references where those are higher, and scales its sums and O^T so far.  Returns
-// whether a reference is a big one.
+// This group of four warps raises its columns' references to the maxima of this
+// tile's scores where those are higher, and scales its sums and O^T so far.  Returns
+// whether a reference is a raw score.
 template <int D, int N>
 __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bool plain, bool all, uint64_t bit, float sl,
                                      int c0, int quad, int lane, int bar, bool started, f32x2 (&l)[N / 4],
@@ -641,19 +672,31 @@ __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
 {
     using L = Plan<D, N>;
     constexpr int C = L::kCols;
+    const float sign = sl < 0.f ? -1.f : 1.f;
 #pragma unroll 1
     for (int i0 = 0; i0 < C; i0 += 8) {
         float x[8];
         tm_ld(at_s + i0, x);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float v = plain || all || (s.vis[c0 + i0 + i] & bit) ? x[i] * sl : -INFINITY;
+            float v = plain || all || (s.vis[c0 + i0 + i] & bit) ? x[i] * sign : -INFINITY;
 #pragma unroll
             for (int o = 16; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
             if (lane == 0) s.red[quad][c0 + i0 + i] = v;
         }
     }
     any_of(bar, 128, false);
+    bool raw = false;
+    if (quad * 32 + lane < C) {
+        const int col = c0 + quad * 32 + lane;
+        const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
+        float down;
+        const Reference now = raised(Reference{s.neg_m[col], s.raw[col] != 0}, top, sl, down);
+        s.inv[col] = down == 0.f ? 1.f : fast_exp2(down);
+        s.neg_m[col] = now.neg;
+        s.raw[col] = raw = now.raw;
+    }
+    raw = any_of(bar, 128, raw);
     // O^T so far, once every product before this tile is done
     if (started) {
         fail = fail || !waitw(pfree, parity, abort);
@@ -663,13 +706,7 @@ __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
     for (int i0 = 0; i0 < C; i0 += 8) {
         float down[8];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int col = c0 + i0 + j;
-            const float was = -s.neg_m[col];
-            const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-            const float now = fmaxf(reference_of(top), was);
-            down[j] = was == now ? 1.f : fast_exp2(was - now);
-        }
+        for (int j = 0; j < 8; ++j) down[j] = s.inv[c0 + i0 + j];
 #pragma unroll
         for (int j = 0; j < 8; j += 2) {
             float v, w;
@@ -690,16 +727,7 @@ __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
         }
     }
     fence_before();
-    any_of(bar, 128, false);  // every thread has read the old references
-    const int col = c0 + quad * 32 + lane;
-    bool big = false;
-    if (quad * 32 + lane < C) {
-        const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-        const float now = fmaxf(-s.neg_m[col], reference_of(top));
-        s.neg_m[col] = -now;
-        big = is_big(now);
-    }
-    return any_of(bar, 128, big);
+    return raw;
 }
 
 // ------------------------------------------------- what both kernels share
@@ -987,6 +1015,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 }
                 s.vis[tid] = w;
                 s.neg_m[tid] = 0.f;
+                s.raw[tid] = 0;
                 if (tid == 0) s.bad_v = 0;
             }
             any_of(kAllBar, kSoftThreads, false);
@@ -994,7 +1023,7 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
             f32x2 l[C / 2];
 #pragma unroll
             for (int i = 0; i < C / 2; ++i) l[i] = 0;
-            bool stop = false, big = false;
+            bool stop = false, some_raw = false;
             for (int t = 0; t < n; ++t) {
                 const int T = done + t, sb = T & 1, pb = T % L::kPBufs;
                 const int slot = (g.t0 + t) * kTile + srow;
@@ -1008,11 +1037,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fail = fail || !waitw(smem_addr(&s.sfull[sb]), (T >> 1) & 1, abort);
                 fence_after();
                 float x[C];
-                read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
-                if (t == 0)
-                    big = first_references<C>(s, x, c0, quad, lane, bar);
-                else if (big)
-                    cut<C>(x);
+                read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0, some_raw, s.raw + c0);
+                if (t == 0) first_references<C>(s, x, c0, quad, lane, bar);
                 // Two buffers of P: S of this tile was issued after O of the tile before the
                 // last, so once S is there the weights of that tile are done with.
                 if (L::kPBufs == 1 && T > 0) fail = fail || !waitw(smem_addr(&s.pfree[0]), (T - 1) & 1, abort);
@@ -1020,16 +1046,15 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 // The weights are formed before it is known whether the references hold
                 // (the maxima hide behind the exponentials); if not, again.
                 const float over = weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
-                if (any_of(bar, 128, over > kHeadroom || fail)) {
+                if (any_of(bar, 128, over > kMostLog || fail)) {
                     if (any_of(bar, 128, fail)) {
                         if (lane == 0) give_up(abort);
                         stop = true;
                         break;
                     }
-                    big = rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
+                    some_raw = rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
                                smem_addr(&s.pfree[(T + L::kPBufs - 1) % L::kPBufs]), ((T - 1) / L::kPBufs) & 1, abort, fail);
-                    read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0);
-                    if (big) cut<C>(x);
+                    read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0, some_raw, s.raw + c0);
                     weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
                 }
 #pragma unroll
@@ -1076,10 +1101,11 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 const float sum = (s.red[0][tid] + s.red[1][tid]) + (s.red[2][tid] + s.red[3][tid]);
                 s.inv[tid] = sum == 0.f ? 0.f : 1.f / sum;
                 if (tid < rows) {
+                    const Reference m = {s.neg_m[tid], s.raw[tid] != 0};
                     if (!whole)
-                        p.part_ml[part * N + tid] = make_float2(-s.neg_m[tid], sum);
+                        p.part_ml[part * N + tid] = make_float2(-m.neg, m.raw ? -sum : sum);
                     else if (a.lse)
-                        a.lse[s.lse[tid]] = sum == 0.f ? -INFINITY : (log2f(sum) - s.neg_m[tid]) * 0.6931471805599453f;
+                        a.lse[s.lse[tid]] = log_sum(sum, m, sl);
                 }
             }
             any_of(kAllBar, kSoftThreads, false);
@@ -1140,12 +1166,9 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
 
 // ---------------------------------------------------- many rows to a head
 
-// 32 of a row's scores as log2 weights, x = s scale log2(e) + neg_m; those not in `seen` -inf.
-__device__ __forceinline__ void log2_weights(float (&x)[32], float sl, float neg_m, bool plain, uint32_t seen)
+// What is not in `seen` becomes -inf.
+__device__ __forceinline__ void unseen_out(float (&x)[32], bool plain, uint32_t seen)
 {
-    const f32x2 scale = pair(sl, sl), minus = pair(neg_m, neg_m);
-#pragma unroll
-    for (int i = 0; i < 32; i += 2) unpair(fma2(pair(x[i], x[i + 1]), scale, minus), x[i], x[i + 1]);
     if (!plain) {
 #pragma unroll
         for (int i = 0; i < 32; ++i)
@@ -1153,15 +1176,32 @@ __device__ __forceinline__ void log2_weights(float (&x)[32], float sl, float neg
     }
 }
 
-// The largest of a row's 64 log2 scores.
+// 32 of a row's scores as log2 weights, x = s scale log2(e) - m; those not in `seen` -inf.
+__device__ __forceinline__ void log2_weights(float (&x)[32], float sl, Reference m, bool some_raw, bool plain, uint32_t seen)
+{
+    if (some_raw) {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] = m.raw ? raw_weight(x[i], m.neg, sl) : fmaf(x[i], sl, m.neg);
+    } else {
+        const f32x2 scale = pair(sl, sl), minus = pair(m.neg, m.neg);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) unpair(fma2(pair(x[i], x[i + 1]), scale, minus), x[i], x[i + 1]);
+    }
+    unseen_out(x, plain, seen);
+}
+
+// The largest of a row's 64 scores, times the scale's sign.
 __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, const uint32_t (&seen)[2])
 {
+    const float sign = sl < 0.f ? -1.f : 1.f;
     float top = -INFINITY;
 #pragma unroll 1
     for (int c = 0; c < 2; ++c) {
         float x[32];
         tm_ld(at + 32 * c, x);
-        log2_weights(x, sl, 0.f, plain, c == 0 ? seen[0] : seen[1]);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) x[i] *= sign;
+        unseen_out(x, plain, c == 0 ? seen[0] : seen[1]);
 #pragma unroll
         for (int i = 0; i < 32; i += 2) top = max3(top, x[i], x[i + 1]);
     }
@@ -1169,8 +1209,8 @@ __device__ __forceinline__ float row_top(uint32_t at, float sl, bool plain, cons
 }
 
 // A row's weights as packed bf16 pairs; returns their sum (before the rounding).
-__device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, bool plain, const uint32_t (&seen)[2],
-                                           bool big, uint32_t (&w)[32])
+__device__ __forceinline__ float weigh_row(uint32_t at, float sl, Reference m, bool some_raw, bool plain,
+                                           const uint32_t (&seen)[2], uint32_t (&w)[32])
 {
     f32x2 s0 = 0, s1 = 0;
     float buf[2][32];
@@ -1185,8 +1225,7 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, float neg_m, b
             tm_ld16(at + 32, buf[1]);
             tm_ld16(at + 48, buf[1] + 16);
         }
-        log2_weights(x, sl, neg_m, plain, seen[z]);
-        if (big) cut<32>(x);
+        log2_weights(x, sl, m, some_raw, plain, seen[z]);
 #pragma unroll
         for (int i = 0; i < 32; i += 4) {
 #pragma unroll
@@ -1434,8 +1473,9 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                 }
             };
             pages_of(0);
-            float neg_m = 0.f, l = 0.f;
-            bool big = false;  // a reference of the warp's is
+            Reference m = {-kUnseen, false};
+            float l = 0.f;
+            bool some_raw = false;  // a reference of the warp's is
             for (int st = 0; st < steps; ++st) {
                 const int slot0 = g.t0 * kTile + st * kStep, S = did + st;
                 const uint32_t at_s = at_half + S % 2 * kStep;
@@ -1465,19 +1505,18 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                 fence_after();
                 uint32_t w[kStep / 2];
                 float sum;
-                // The first step's largest scores are the references; later ones rise where a
-                // score passes them by more than the headroom: then the weights' sum is above
-                // 2^kHeadroom, which costs nothing to see.
+                // The references go by the first step's largest scores; later they rise where the
+                // weights' sum is above kMostWeight, which costs nothing to see.
                 bool rise = st == 0;
 #pragma unroll 1
                 for (int turn = 0; turn < 2; ++turn) {
                     if (__any_sync(0xffffffffu, rise)) {
-                        const float was = st == 0 && turn == 0 ? kUnseen : -neg_m, top = row_top(at_s, sl, plain, seen);
-                        const float now = rise ? fmaxf(reference_of(top), was) : was;
-                        const float down = was == now ? 1.f : fast_exp2(was - now);
+                        const float top = row_top(at_s, sl, plain, seen);
+                        float down = 0.f;
+                        if (rise) m = raised(m, top, sl, down);
+                        down = down == 0.f ? 1.f : fast_exp2(down);
                         l *= down;
-                        neg_m = -now;
-                        big = __any_sync(0xffffffffu, is_big(now));
+                        some_raw = __any_sync(0xffffffffu, m.raw);
                         if (st > 0) {
                             // O so far, once the step before is in (S waited for the one before that)
                             ok = ok && waitw(smem_addr(&s.pfree[half]), (S - 1) & 1, abort);
@@ -1492,7 +1531,7 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
                             }
                         }
                     }
-                    sum = weigh_row(at_s, sl, neg_m, plain, seen, big, w);
+                    sum = weigh_row(at_s, sl, m, some_raw, plain, seen, w);
                     rise = sum > kMostWeight;
                     if (!__any_sync(0xffffffffu, rise)) break;
                 }
@@ -1514,9 +1553,9 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
             const float inv = l == 0.f ? 0.f : 1.f / l;
             if (col < rows) {
                 if (!whole)
-                    p.part_ml[part] = make_float2(-neg_m, l);
+                    p.part_ml[part] = make_float2(-m.neg, m.raw ? -l : l);
                 else if (a.lse)
-                    a.lse[(lo + i) * a.q_heads + head] = l == 0.f ? -INFINITY : (log2f(l) - neg_m) * 0.6931471805599453f;
+                    a.lse[(lo + i) * a.q_heads + head] = log_sum(l, m, sl);
             }
             const uint64_t badv = s.bad_v & vis;
             uint16_t* out = (uint16_t*)a.out + (int64_t)(lo + i) * a.ldo + (int64_t)head * D;
@@ -1574,8 +1613,11 @@ __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
 // order: a warp per (row, head), all warps of the GPU at once.  (The last CTA
 // of a pair joining it in the first kernel took 20 us and more for twelve parts
 // of 48 x 256: one SM's loads.)
+// The bounds are the registers that eight loads in flight take: at the compiler's own
+// choice of 32 to 48 it spills (1 lane x 16 rows, 64 / 8 heads of 64, 65,537 slots 61.3 us,
+// at 64 registers 59.3; 32 rows, 16 / 4 heads of 256, 40,000 slots 59.6, at 80 53.9).
 template <int D, int N>
-__global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ AttnParams p)
+__global__ void __launch_bounds__(256, D == 256 ? 3 : 4) attn_join_kernel(const __grid_constant__ AttnParams p)
 {
     __shared__ Lanes s;
     const nvfp4_attn_args& a = p.a;
@@ -1605,10 +1647,37 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
     const int64_t rest = ((int64_t)(glo * s.width + blk) * 2) * N + col, step = (int64_t)s.width * 2 * N;
     auto at = [&](int q) { return q ? rest + q * step : rest + lo_slot * N; };
     constexpr int kPer = D / 32;  // values per lane
-    float top = kUnseen;
-    for (int q = lane; q < np; q += 32) top = fmaxf(top, __ldcg(&p.part_ml[at(q)]).x);
+    // The highest reference m, and the highest u = r sign(sl) of the raw ones: those above
+    // zero lie above every m, the others below (but above a part that saw nothing).
+    const float sl = a.scale * 1.4426950408889634f, mag = fabsf(sl);
+    auto u_of = [&](float r) { return sl < 0.f ? -r : r; };
+    float top = kUnseen, top_u = -INFINITY;
+    bool raws = false;
+    for (int q = lane; q < np; q += 32) {
+        const float2 ml = __ldcg(&p.part_ml[at(q)]);
+        if (signbit(ml.y)) {
+            raws = true;
+            top_u = fmaxf(top_u, u_of(ml.x));
+        } else {
+            top = fmaxf(top, ml.x);
+        }
+    }
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    raws = __any_sync(0xffffffffu, raws);
+    if (raws) {
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) top_u = fmaxf(top_u, __shfl_xor_sync(0xffffffffu, top_u, o));
+    }
+    const bool raw = top_u > 0.f || (top == kUnseen && top_u > -INFINITY);
+    // log2 factor of a part's weights against the highest reference, as in raised()
+    auto factor = [&](float2 ml) {
+        if (raws && signbit(ml.y)) {
+            const float u = u_of(ml.x);
+            return raw ? (u - top_u) * mag : fmaf(u, mag, -top) + kAbove;
+        }
+        return raw ? -(fmaf(top_u, mag, -ml.x) + kAbove) : ml.x == top ? 0.f : ml.x - top;
+    };
     float sum = 0.f, acc[kPer];
 #pragma unroll
     for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
@@ -1616,8 +1685,8 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         float w = 0.f;
         if (q0 + lane < np) {
             const float2 ml = __ldcg(&p.part_ml[at(q0 + lane)]);
-            w = ml.x == top ? 1.f : fast_exp2(ml.x - top);
-            sum += ml.y * w;
+            w = fast_exp2(factor(ml));
+            sum += fabsf(ml.y) * w;
         }
         const int n = min(32, np - q0);
 #pragma unroll 8
@@ -1652,7 +1721,7 @@ __global__ void __launch_bounds__(256) attn_join_kernel(const __grid_constant__ 
         out[d / 2] = *reinterpret_cast<const uint32_t*>(&h);
     }
     if (lane == 0 && a.lse)
-        a.lse[(int64_t)r * a.q_heads + head] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+        a.lse[(int64_t)r * a.q_heads + head] = log_sum(sum, raw ? Reference{-u_of(top_u), true} : Reference{-top, false}, sl);
 }
 
 // ------------------------------------------------------------------- host
