@@ -533,8 +533,12 @@ NVFP4_API int nvfp4_attn_tree_workspace(int rows, int q_heads, int kv_heads, int
  *   candidate(w, v) = scores[m] + logits[m][v] - log sum_u exp(logits[m][u]),
  * and the group's `beams` best candidates, best first, go to
  *   scores_out[g * beams + j], parent[...] = the row m it extends, token[...] = v.
- * Candidates are compared in 64 bits, equal ones by lower w * V + v, and the
- * score is rounded once.  finished (u8 [rows], or NULL): a beam with a nonzero
+ * Candidates are compared by 64-bit sums, equal ones by lower w * V + v, and the
+ * score is rounded once.  The logarithm in them is of a sum of 32-bit exponentials:
+ * off by 2^-16 at most, by some 2^-22 for rows of a model.  So a beam's own
+ * candidates rank exactly as their logits do, as do those of beams with equal
+ * rows; of candidates of different rows that lie nearer to one another than that,
+ * either may come first, the same one in every call.  finished (u8 [rows], or NULL): a beam with a nonzero
  * entry has one candidate, token eos at its score as it is; finished_out (u8
  * [rows], or NULL) is 1 where the parent was finished or the token is eos.
  * Candidates of score -inf (masked logits, beams whose score is -inf) and NaN
