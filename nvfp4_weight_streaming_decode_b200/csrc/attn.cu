@@ -501,10 +501,10 @@ __device__ __forceinline__ Segment segment_at(const Lanes& s, int lanes, int u, 
 __device__ __forceinline__ int pos_k(int t) { return t == 0 ? 0 : 2 * t - 1; }
 __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 2 : 2 * n - 1; }
 
-// A log2 weight is s sl - m, one rounding; but m is a rounded score, and so is s sl
-// where the first tile's maximum is looked for.  From kRaw on, where that would
-// show (by 2^-12), a reference is a raw score r (before the scale) instead:
-// the weight is (s - r) sl - kAbove, and s - r is exact for the scores that count.
+// A log2 weight is s sl - m, one rounding; but m is a rounded score, so the largest
+// weight may be off 2^-kAbove by that.  From kRaw on, long before that would show,
+// a reference is a raw score r (before the scale) instead: the weight is
+// (s - r) sl - kAbove, and s - r is exact for the scores that count.
 constexpr float kRaw = 4096.f;
 __device__ __forceinline__ bool is_raw(float top) { return fabsf(top) >= kRaw && fabsf(top) < -kUnseen; }
 __device__ __forceinline__ float raw_weight(float s, float neg_r, float sl) { return (s + neg_r) * sl - kAbove; }
@@ -639,12 +639,12 @@ __device__ __forceinline__ void join_columns(const float (&x)[C], int lane, floa
     }
 }
 
-// The first tile of a segment: its columns' maxima become the references, and
-// the scores (read with references of 0) are taken against them.  A column
-// that sees nothing yet stays unseen, and so does one whose reference has to be a raw
-// score: its weights then show as too large, and rise() sees to it.
+// The first tile of a segment: its columns' maxima (of scores read with references of
+// 0) become the references.  A column that sees nothing yet stays unseen, and so
+// does one whose reference has to be a raw score: its weights then show as too
+// large, and rise() sees to it.
 template <int C>
-__device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c0, int quad, int lane, int bar)
+__device__ __forceinline__ void first_references(Shared& s, const float (&x)[C], int c0, int quad, int lane, int bar)
 {
     join_columns<C>(x, lane, s.red[quad] + c0, [](float a, float b) { return fmaxf(a, b); });
     any_of(bar, 128, false);
@@ -654,16 +654,11 @@ __device__ __forceinline__ void first_references(Shared& s, float (&x)[C], int c
         s.neg_m[col] = -(is_raw(top) ? kUnseen : fmaxf(top + kAbove, kUnseen));
     }
     any_of(bar, 128, false);
-#pragma unroll
-    for (int i = 0; i < C; i += 4) {
-        const ulonglong2 m = *reinterpret_cast<const ulonglong2*>(s.neg_m + c0 + i);
-        unpair(add2(pair(x[i], x[i + 1]), m.x), x[i], x[i + 1]);
-        unpair(add2(pair(x[i + 2], x[i + 3]), m.y), x[i + 2], x[i + 3]);
-    }
 }
 
-// This group of four warps raises its columns' references to the maxima of this
-// tile's scores where those are higher, and scales its sums and O^T so far.  Returns
+// This group of four warps raises the references of the columns with a weight above
+// 2^kMostLog in this tile, those alone (a row's result does not depend on the others'),
+// to the maxima of the tile's scores, and scales its sums and O^T so far.  Returns
 // whether a reference is a raw score.
 template <int D, int N>
 __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bool plain, bool all, uint64_t bit, float sl,
@@ -690,8 +685,11 @@ __device__ __forceinline__ bool rise(Shared& s, uint32_t at_s, uint32_t at_o, bo
     if (quad * 32 + lane < C) {
         const int col = c0 + quad * 32 + lane;
         const float top = fmaxf(fmaxf(s.red[0][col], s.red[1][col]), fmaxf(s.red[2][col], s.red[3][col]));
-        float down;
-        const Reference now = raised(Reference{s.neg_m[col], s.raw[col] != 0}, top, sl, down);
+        float down = 0.f;
+        Reference now = {s.neg_m[col], s.raw[col] != 0};
+        // the largest weight, as read_scores has it
+        if ((now.raw ? raw_weight(top * sign, now.neg, sl) : fmaf(top * sign, sl, now.neg)) > kMostLog)
+            now = raised(now, top, sl, down);
         s.inv[col] = down == 0.f ? 1.f : fast_exp2(down);
         s.neg_m[col] = now.neg;
         s.raw[col] = raw = now.raw;
@@ -1037,16 +1035,22 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                 fail = fail || !waitw(smem_addr(&s.sfull[sb]), (T >> 1) & 1, abort);
                 fence_after();
                 float x[C];
-                read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0, some_raw, s.raw + c0);
-                if (t == 0) first_references<C>(s, x, c0, quad, lane, bar);
                 // Two buffers of P: S of this tile was issued after O of the tile before the
                 // last, so once S is there the weights of that tile are done with.
                 if (L::kPBufs == 1 && T > 0) fail = fail || !waitw(smem_addr(&s.pfree[0]), (T - 1) & 1, abort);
                 uint8_t* prow = sm + L::kOffP + pb * L::kPBytes + (srow >> 3) * 128 + (srow & 7) * 16;
-                // The weights are formed before it is known whether the references hold
-                // (the maxima hide behind the exponentials); if not, again.
-                const float over = weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
-                if (any_of(bar, 128, over > kMostLog || fail)) {
+                // Turn 0: the first tile's references.  The weights are formed before it is
+                // known whether the references hold (the maxima hide behind the
+                // exponentials); if not, again in turn 2.
+#pragma unroll 1
+                for (int turn = t == 0 ? 0 : 1;; ++turn) {
+                    read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0, some_raw, s.raw + c0);
+                    if (turn == 0) {
+                        first_references<C>(s, x, c0, quad, lane, bar);
+                        continue;
+                    }
+                    const float over = weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
+                    if (turn == 2 || !any_of(bar, 128, over > kMostLog || fail)) break;
                     if (any_of(bar, 128, fail)) {
                         if (lane == 0) give_up(abort);
                         stop = true;
@@ -1054,9 +1058,8 @@ __global__ void __launch_bounds__(Plan<D, N>::kThreads, 1)
                     }
                     some_raw = rise<D, N>(s, at_s, tm_o + c0 + lanebits, plain, all, bit, sl, c0, quad, lane, bar, t > 0, l,
                                smem_addr(&s.pfree[(T + L::kPBufs - 1) % L::kPBufs]), ((T - 1) / L::kPBufs) & 1, abort, fail);
-                    read_scores<C>(at_s, x, plain, all, bit, sl, s.vis + c0, s.neg_m + c0, some_raw, s.raw + c0);
-                    weigh<C>(x, prow + (c0 >> 3) * (kTile * 16));
                 }
+                if (stop) break;
 #pragma unroll
                 for (int i = 0; i < C / 2; ++i) l[i] = add2(l[i], pair(x[2 * i], x[2 * i + 1]));
                 if (!plain) {

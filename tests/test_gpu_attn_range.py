@@ -158,3 +158,25 @@ def test_scores_from_far_below_zero_to_far_above(dev, n, dim, rows, hq, pattern)
         assert (np.abs(got[i] - want) <= tol).all(), (i, np.max(np.abs(got[i] - want) / tol))
         top = s.max() + np.log(w.sum())
         assert np.abs(gl[i] - top).max() <= 2.0**-21 * (abs(top) + 100)
+
+
+@pytest.mark.parametrize("power", [3, 6, 10, 18, 40])
+@pytest.mark.parametrize("rows,hq", BLOCKS)
+@pytest.mark.parametrize("n,dim", [(0, 128), (100, 64), (300, 256), (9000, 128)])
+def test_a_row_does_not_depend_on_the_others(dev, n, dim, rows, hq, power):
+    """Bit for bit, whatever the scores of the rows beside it: theirs times 2^power, and values that they alone see."""
+    rng = np.random.default_rng(9)
+    c, r = ch.make(dev, 9, [n], [rows], hkv=1, page=16, dim=dim)
+    x = rng.standard_normal((rows, hq, dim))
+    mask = [1 << i | 1 for i in range(rows)]
+    kw = dict(row_start=ch.ints([0, rows], dev), mask=ch.words(mask, dev), max_nodes=rows, want_lse=True)
+    out, lse = abi.attn_tree(c, 0, ch.dev_bf16(cache_ref.bf16_bits(x), dev), dim**-0.5, **kw)
+    x[1::2] *= 2.0**power
+    for i in range(1, rows, 2):
+        p, o = r.where(0, n + i)
+        r.v[0, p, 0, o] = cache_ref.bf16_bits(np.full(dim, 3e38))
+    c2 = ch.device_cache(dev, r.k, r.v, r.table, r.len, r.ref)
+    out2, lse2 = abi.attn_tree(c2, 0, ch.dev_bf16(cache_ref.bf16_bits(x), dev), dim**-0.5, **kw)
+    torch.cuda.synchronize()
+    assert torch.equal(out[::2], out2[::2]) and torch.equal(lse[::2], lse2[::2])
+    assert torch.isfinite(out2).all() and torch.isfinite(lse2).all()
