@@ -401,8 +401,10 @@ NVFP4_API int nvfp4_cache_fork(const nvfp4_cache* cache, const int32_t* parent, 
  * lowest id first, lane by lane, a lane's in the order of its slots.  want:
  * device int32 [lanes], <= 0: nothing.
  * All or nothing: if the pool has too few free pages, or a lane would pass
- * max_pages, nothing changes, bit 256 of nvfp4_device_status() is set and *ok
- * is 0 (else 1).  ok: device int32, or NULL.  One asynchronous launch.
+ * max_pages, nothing changes and bit 256 of nvfp4_device_status() is set.  A lane
+ * with a page id outside the pool under those slots, or no page under its partly
+ * filled last one, is left as it was (bit 128).  *ok is 1 if every lane has its
+ * room, else 0.  ok: device int32, or NULL.  One asynchronous launch.
  */
 NVFP4_API int nvfp4_cache_reserve(const nvfp4_cache* cache, const int32_t* want, int32_t* ok, nvfp4_stream_t stream);
 

@@ -546,7 +546,7 @@ class Cache:
 
     def reserve(self, want, ok=None, stream=None):
         """Room for want[b] more slots in each lane, in pages of its own: shared ones are copied or replaced.
-        ok: int32 [1], set to 0 if the pool had too few free pages."""
+        ok: int32 [1], set to 1 if every lane has its room, to 0 if not (too few free pages: nothing changes)."""
         import torch
         wp, op = self._lanes(want, "want"), _want(ok, "ok", torch.int32, self.device, (1,))
         _call("nvfp4_cache_reserve", self.device, stream, self._ref, wp, op)

@@ -86,7 +86,7 @@ struct Plan {
     int start[kMaxLanes + 1];  // pages taken before lane b
     int ids[kResStep];         // the free pages of a step, where entries are replaced
     int count[kResWarps];
-    int bad, copies, replaces, last_in;
+    int bad, left, copies, replaces, last_in;
 };
 
 // Whether lane b gives up page p, in its column col: another holder is left when the
@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
     const int shift = __ffs(c.page_size) - 1;
     if (tid == 0) {
         s.bad = 0;
+        s.left = 0;
         s.copies = 0;
         s.replaces = 0;
     }
@@ -221,28 +222,29 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
         const int c0 = (n + c.page_size - 1) >> shift, c1 = (int)((end + c.page_size - 1) >> shift);
         const bool partly = n & (c.page_size - 1);
         const int p = partly ? row[n >> shift] : -1;
+        bool bad = partly && (p < 0 || p >= c.pages);
         int first = c1;  // entries from here on are -1: a lane's pages come first
         for (int q = c0; q < c1; q += 32) {
             const int e = q + lane < c1 ? row[q + lane] : 0;
             const unsigned m = __ballot_sync(0xffffffffu, e < 0);
+            bad = bad || __any_sync(0xffffffffu, e >= c.pages && (m == 0 || lane < __ffs(m)));
             if (m) {
                 first = q + __ffs(m) - 1;
                 break;
             }
         }
-        if (lane == 0) {
+        if (bad) {  // a slot would have no page, or one outside the pool: the lane is left out
+            if (lane == 0) {
+                s.left = 1;
+                if (blockIdx.x == 0) atomicOr(&g_cache_status, kRefused);
+            }
+        } else if (lane == 0) {
             s.need[b] = c1 - first;
             s.lo[b] = s.at[b] = c0;
             s.first[b] = first;
             s.fill[b] = n & (c.page_size - 1);
             s.col[b] = n >> shift;
-            if (partly) {
-                if (p >= 0 && p < c.pages) {
-                    s.last[b] = p;
-                } else if (blockIdx.x == 0) {
-                    atomicOr(&g_cache_status, kRefused);
-                }
-            }
+            s.last[b] = p;
         }
     }
     __syncthreads();
@@ -362,7 +364,7 @@ __global__ void __launch_bounds__(kResThreads) reserve_kernel(const nvfp4_cache 
     }
     if (enough && tid < c.lanes && s.copy[tid]) atomicSub(c.ref + s.last[tid], 1);
     if (tid == 0) {
-        if (ok) *ok = enough ? 1 : 0;
+        if (ok) *ok = enough && !s.left ? 1 : 0;
         if (!enough) atomicOr(&g_cache_status, kNoPages);
         if (s.copies || s.replaces) *counter = 0u;
     }

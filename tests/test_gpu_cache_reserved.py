@@ -203,3 +203,29 @@ def test_a_captured_reserve_replays(dev):
         assert r.reserve([20] * n) and own(r, [20] * n)
         r.compact([20] * n)
         ch.assert_same(c, r)
+
+
+@pytest.mark.parametrize("col,entry", [(1, -1), (1, 1 << 24), (2, 1 << 20), (3, 2**31 - 1)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_a_lane_with_a_bad_page_there_is_left_as_it_was(dev, col, entry, shared):
+    """No page under a partly filled last one, or an id outside the pool under the slots asked for: no room, and told
+    so; the other lanes get theirs."""
+    c, r = ch.make(dev, 9, [10, 20, 17], [0, 40, 0], layers=2, spare=12, width_extra=3)
+    t = lambda a: ch.ints(a, dev)  # noqa: E731
+    if shared:
+        for x, u in ((c, t), (r, list)):
+            x.fork(u([0, 1, 0]))
+    kept = int(r.table[1, col])
+    c.table[1, col] = entry
+    ok = torch.full((1,), 7, dtype=torch.int32, device=dev)
+    c.reserve(t([30, 40, 30]), ok)
+    assert r.reserve([30, 0, 30])
+    torch.cuda.synchronize()
+    assert ok.item() == 0 and ch.clean_status() == 128
+    c.table[1, col] = kept
+    ch.assert_same(c, r)
+    # not under the slots asked for, it does not matter
+    c.table[1, 3] = 1 << 24
+    c.reserve(t([0, 5, 0]), ok)
+    torch.cuda.synchronize()
+    assert ok.item() == 1
