@@ -48,11 +48,13 @@
 // take 1,024, and the operands' way through shared memory about as much as the
 // products); for short contexts the chain of one tile's steps.  Measured
 // (device time of a call, join included; the fraction is of 6,530 GB/s copied):
-//   8 lanes x 1 row, 40 / 40 heads of 128, up to 4,000 slots   80 us  5.7 TB/s 0.87
-//   8 lanes x 8 rows, 40 / 8 heads of 128, up to 32,768 slots 125 us  5.9 TB/s 0.91
-//   5 lanes x 2-8 rows, 24 / 4 heads of 256, up to 20,011      57 us  4.9 TB/s 0.75
-//   1 row, 40 / 8 heads, no context                           7.4 us
-//   1 lane x 64 rows, 64 / 8 heads of 128, 65,537 slots       136 us  1.01 PFLOP/s (attn_wide_kernel)
+//   8 lanes x 1 row, 40 / 40 heads of 128, up to 4,000 slots   78 us  5.8 TB/s 0.89
+//   8 lanes x 8 rows, 40 / 8 heads of 128, up to 32,768 slots 123 us  6.0 TB/s 0.92
+//   5 lanes x 2-8 rows, 24 / 4 heads of 256, up to 20,011      56 us  4.9 TB/s 0.76
+//   1 row, 40 / 8 heads, no context                           7.1 us
+//   1 lane x 64 rows, 64 / 8 heads of 128, 65,537 slots       135 us  1.02 PFLOP/s (attn_wide_kernel; 161 us and
+//                                                             0.86 PFLOP/s in a long run, under the power limit)
+//   1 lane x 16 rows, 64 / 8 heads of 64, 65,537 slots         57 us  2.3 TB/s 0.36 (blocks of 128 rows: the softmax)
 //
 // Every wait is bounded; one that runs out flags the device status, stops the
 // CTA, waits (bounded) for copies and products in flight, frees the tensor
@@ -1259,18 +1261,26 @@ __device__ __forceinline__ float weigh_row(uint32_t at, float sl, Reference m, b
 // V is shared, so one more warp looks after its slots that rows must not see, ahead
 // of the products.
 //
-// Measured against blocks of 128 rows in attn_kernel (64 query heads, 8 cached of
-// 128, one lane): 64 rows of 65,537 slots 136 us and 177, 32 rows 85 and 99, 20 rows
-// 82 and 98, 48 rows (a block and a half) 144 and 140; 64 rows of 4,000 slots 28.8 and
-// 28.8, 1,000 slots 24.1 and 26.5; 20 rows of 4,000 slots 23.8 and 23.1; heads of 64, 64 rows 118 and 177.
-// So any lane of more than 128 rows to a head comes here.
+// Measured against blocks of 128 rows in attn_kernel (64 query heads, 8 cached ones,
+// one lane; us here and there):
+//              heads of 128                        heads of 64
+//   slots      20 rows   32     48      64         20 rows   32     48      64
+//    1,000     22  22  20  20  22  26  23  27      20  21  16  18  19  24  19  25
+//    4,000     22  21  24  21  27  25  28  27      18  20  19  20  22  24  22  26
+//   16,000     35  38  38  39  51  49  50  59      30  36  31  37  42  47  43  57
+//   65,537     78  97  81  97 136 140 135 179      68  96  69  97 122 140 120 181
+// Heads of 128 with a block and a half lose up to 10 % between 4,000 and 16,000 slots, as
+// does a full block at 4,000; everything else gains, up to 30 %.  The lengths are not known
+// where the kernel is chosen, so any lane of more than 128 rows to a head comes here.
 //
-// Bound by the loop of weights, products and scores: a step of 64 slots for both
-// halves takes 1,860 cycles, the exponentials 1,024 of them and the products 1,024
-// (51 % of the tensor and of the exponential unit's cycles); leaving out the
-// exponentials changes nothing, leaving out the products 10 %.  Runs of some
-// milliseconds meet the power limit (160 us).  Not kept: a warp of products for each
-// half, waits that poll, other orders of the halves (140 to 146 us).
+// Bound by the softmax warps' own chain: a step of 64 slots for both halves takes
+// 1,860 cycles, of which the exponentials and the products take 1,024 each (52 % of
+// either unit's cycles), and leaving out the exponentials changes nothing, the
+// products 10 %.  A warp's step is page lookup and ballots, the wait for the scores, their
+// loads, packing, the store and its wait, one after the other, and there are two warps to
+// a quarter of the SM to hide it.  Runs of some milliseconds meet the power limit (161 us).
+// Not kept: a warp of products for each half, waits that poll, other orders of
+// the halves (140 to 146 us).
 template <int D>
 __global__ void __launch_bounds__(Plan<D, 256>::kThreads, 1)
     attn_wide_kernel(const __grid_constant__ AttnParams p, const __grid_constant__ CUtensorMap map_k,

@@ -583,7 +583,7 @@ extern "C" int nvfp4_cache_compact(const nvfp4_cache* cache, const int32_t* coun
     auto launch = [&](auto kernel, int D) {
         const int64_t groups = kMoveThreads / (D / 8), segs = (int64_t)cache->layers * 2 * cache->kv_heads;
         int64_t gx = (segs + groups - 1) / groups;
-        const int64_t cap = (8 * sms + cache->lanes - 1) / cache->lanes;  // one wave of resident CTAs
+        const int64_t cap = (8 * sms + cache->lanes - 1) / cache->lanes;  // about 8 CTAs an SM, of which 3 are resident
         if (gx > cap) gx = cap;
         const dim3 grid = path ? dim3((unsigned)gx, (unsigned)cache->lanes) : dim3(1, (unsigned)cache->lanes);
         return launch_pdl(kernel, grid, dim3(kMoveThreads), 0, stream, *cache, count, path, ld_path);
