@@ -84,7 +84,8 @@ constexpr float kAbove = 24.f;             // a reference lies this far above it
 constexpr float kUp = 16777216.f;          // 2^kAbove
 constexpr float kMostLog = -16.f;          // a score with more than this against its reference raises it
 constexpr float kMostWeight = 1.f / 65536;  // 2^kMostLog
-constexpr float kUnseen = -3.0e38f;        // reference of a column that has seen no slot
+constexpr float kMostFloat = 3.402823466e38f;
+constexpr float kUnseen = -kMostFloat;     // reference of a column that has seen no slot
 constexpr uint32_t kSleepNs = 1000;
 constexpr uint32_t kPolls = 1u << 20;      // about a second
 
@@ -508,7 +509,7 @@ __device__ __forceinline__ int pos_v(int t, int n) { return t + 1 < n ? 2 * t + 
 // a reference is a raw score r (before the scale) instead: the weight is
 // (s - r) sl - kAbove, and s - r is exact for the scores that count.
 constexpr float kRaw = 4096.f;
-__device__ __forceinline__ bool is_raw(float top) { return fabsf(top) >= kRaw && fabsf(top) < -kUnseen; }
+__device__ __forceinline__ bool is_raw(float top) { return fabsf(top) >= kRaw && fabsf(top) <= kMostFloat; }
 __device__ __forceinline__ float raw_weight(float s, float neg_r, float sl) { return (s + neg_r) * sl - kAbove; }
 
 // A column's reference: -m, or -r where raw.

@@ -180,3 +180,26 @@ def test_a_row_does_not_depend_on_the_others(dev, n, dim, rows, hq, power):
     torch.cuda.synchronize()
     assert torch.equal(out[::2], out2[::2]) and torch.equal(lse[::2], lse2[::2])
     assert torch.isfinite(out2).all() and torch.isfinite(lse2).all()
+
+
+@pytest.mark.parametrize("rows,hq", BLOCKS)
+@pytest.mark.parametrize("n,dim", [(0, 128), (300, 64), (300, 256), (9000, 128)])
+def test_scores_at_the_end_of_the_range(dev, n, dim, rows, hq):
+    """Scores of 1.34375 2^127 of either sign (3.3e38 in log2, next to the largest of 32 bits), all alike: the mean of the
+    values a row sees.  Beside them rows of scores 0."""
+    rng = np.random.default_rng(5)
+    total = n + rows
+    keys, q = np.zeros((total, dim)), np.zeros((rows, hq, dim))
+    keys[:, 0] = 1.34375 * 2.0**63
+    q[:, :, 0] = (2.0**64 * np.array([1.0, -1.0, 0.0]))[np.arange(rows) % 3][:, None]
+    values = rng.standard_normal((total, dim))
+    r, _, out, lse = lane(dev, rng, n, rows, dim, keys, values, q, 1.0)
+    t = np.arange(total)
+    v = cache_ref.bf16_value(r.v[0, r.table[0, t // r.page], 0, t % r.page]).astype(np.float64)
+    got, gl = out.float().cpu().numpy(), lse.cpu().numpy()
+    for i in range(rows):
+        m = n + i + 1
+        want, wabs = v[:m].mean(0), np.abs(v[:m]).mean(0)
+        assert (np.abs(got[i] - want) <= wabs * (2.0**-8 + 2 * m * 2.0**-24) * 1.01 + np.abs(want) * 2.0**-8 * 1.01).all(), i
+        top = q[i, 0, 0] * keys[0, 0] + np.log(m)
+        assert np.abs(gl[i] - top).max() <= 2.0**-21 * (abs(top) + 1)
